@@ -13,11 +13,13 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 _CSRC = os.path.join(HERE, "csrc")
 # (source, extra flags): the mixed-format and asymmetric reduces are built once
-# per input format
+# per input format, the products once per weight format
 SOURCES = [(os.path.join(_CSRC, "qr_api.hip"), [])] + [
     (os.path.join(_CSRC, "qr_reduce_mixed.hip"), [f"-DQR_MIXED_IN={b}"]) for b in (3, 4, 8)] + [
     (os.path.join(_CSRC, "qr_asym.hip"), [f"-DQR_ASYM_IN={f}"]) for f in (20, 24)] + [
-    (os.path.join(_CSRC, "qr_fp4.hip"), [])]
+    (os.path.join(_CSRC, "qr_fp4.hip"), [])] + [
+    (os.path.join(_CSRC, "qr_ops.hip"), [])] + [
+    (os.path.join(_CSRC, "qr_product.hip"), [f"-DQR_PRODUCT_FMT={f}"]) for f in (4, 20, 36)]
 LIB = os.path.join(HERE, "libqr.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

@@ -163,9 +163,9 @@ const char* qr_status_string(qr_status s) {
   switch (s) {
     case QR_OK: return "ok";
     case QR_ERR_ARG: return "invalid argument (null pointer or rank count)";
-    case QR_ERR_SIZE: return "value count is not a multiple of 2048 or exceeds QR_MAX_TILES (2^30) tiles";
-    case QR_ERR_ALIGN: return "buffer pointer is not 16-byte aligned";
-    case QR_ERR_UNSUPPORTED: return "unsupported format or dtype";
+    case QR_ERR_SIZE: return "size out of range (a codec call's value count is a multiple of 2048 of at most QR_MAX_TILES (2^30) tiles)";
+    case QR_ERR_ALIGN: return "buffer pointer is not aligned (packed and codec buffers: 16 bytes)";
+    case QR_ERR_UNSUPPORTED: return "unsupported format or type";
     case QR_ERR_ALIAS: return "output buffer overlaps another buffer";
     case QR_ERR_HIP: return "HIP launch error";
   }

@@ -1,0 +1,221 @@
+"""Thin Python binding of the C ABI in ``include/qr_ops.h``: the operators of a
+layer whose weights are held in the 4-bit block formats.
+
+As in ``qr``: argument checks and marshalling only, the work runs in the HIP
+kernels of ``libqr.so`` on the current (or the given) stream, and there is no
+fallback path.
+"""
+import ctypes
+import functools
+
+import torch
+
+from .qr import DTYPES, _check, _fmt, _ptr, _stream, lib, qr_encode
+
+WEIGHT_FORMATS = {4: 32, 20: 128, 36: 32}   # format id -> values that share a scale
+ID_TYPES = {torch.int32: 4, torch.int64: 8}
+
+_bound = None
+
+
+def _lib():
+    """``libqr.so`` with the signatures of the operators."""
+    global _bound
+    if _bound is None or _bound is not lib():
+        L = lib()
+        vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
+        L.qr_weight_bytes.restype = sz
+        L.qr_weight_bytes.argtypes = [i, sz, sz]
+        L.qr_linear.restype = i
+        L.qr_linear.argtypes = [i, i, i, vp, sz, vp, vp, sz, sz, sz, sz, vp]
+        L.qr_experts.restype = i
+        L.qr_experts.argtypes = [i, i, i, vp, sz, sz, vp, vp, vp, vp, sz, sz, sz, sz, sz, vp]
+        L.qr_route_workspace.restype = sz
+        L.qr_route_workspace.argtypes = [sz, sz, sz]
+        L.qr_route.restype = i
+        L.qr_route.argtypes = [vp, i, vp, vp, vp, sz, sz, sz, vp, vp]
+        L.qr_combine.restype = i
+        L.qr_combine.argtypes = [i, vp, sz, sz, vp, vp, vp, sz, sz, sz, sz, vp]
+        _bound = L
+    return _bound
+
+
+@functools.lru_cache(maxsize=1024)
+def _weight_bytes(fid, rows, k):
+    n = int(_lib().qr_weight_bytes(fid, rows, k))
+    if not n:
+        raise ValueError(f"no packed weight of format {fid}, {rows} rows of {k} values")
+    return n
+
+
+def qr_weight_bytes(fmt, rows, k):
+    """Bytes of the packed form of a [rows, k] weight."""
+    return _weight_bytes(_fmt(fmt), int(rows), int(k))
+
+
+def qr_encode_weight(fmt, w, packed=None, stream=None):
+    """Packs the fp16/bf16 device matrix ``w`` [rows, k] (or [experts, rows, k])
+    as the products read it: rows padded with zeros to whole blocks, and the
+    whole to a multiple of 2048 values, then ``qr_encode``."""
+    fid = _fmt(fmt)
+    if fid not in WEIGHT_FORMATS:
+        raise ValueError(f"format {fmt!r} holds no weights (one of int4, asym4, fp4)")
+    if w.dim() < 2:
+        raise ValueError("w must have rows of k values")
+    w = w.reshape(-1, w.shape[-1])
+    rows, k = w.shape
+    nbytes = _weight_bytes(fid, rows, k)
+    group = WEIGHT_FORMATS[fid]
+    kp = -(-k // group) * group
+    n = -(-rows * kp // 2048) * 2048
+    if n != rows * k:
+        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(w.device):
+            flat = torch.zeros(n, dtype=w.dtype, device=w.device)
+            flat[:rows * kp].view(rows, kp)[:, :k] = w
+    else:
+        flat = w.contiguous().view(-1)
+    if packed is None:
+        packed = _empty(nbytes, torch.uint8, w.device, stream)
+    qr_encode(fid, flat, packed, stream)
+    return packed
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor of the stream that will write it: the caching allocator hands
+    memory on in the order of the stream that was current when it was taken."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _matrix(t, name, cols, device, dtype=None):
+    """Address and row stride of a device matrix of ``cols`` neighbouring values a row."""
+    if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
+        raise ValueError(f"{name} must be a device matrix")
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on device {t.get_device()}, the call's tensors are on device {device}")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{name} is {t.dtype}, the call's dtype is {dtype}")
+    rows, have = t.shape
+    ld, step = t.stride()
+    if have != cols:
+        raise ValueError(f"{name} has {have} columns, the call needs {cols}")
+    if have > 1 and step != 1:
+        raise ValueError(f"the values of a row of {name} must be neighbours")
+    if rows < 2:
+        ld = cols
+    elif ld < cols:
+        raise ValueError(f"the rows of {name} must not overlap")
+    return t.data_ptr(), ld
+
+
+def _vector(t, name, numel, dtype, device):
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.numel() != numel:
+        raise ValueError(f"{name} has {t.numel()} values, the call needs {numel}")
+    return _ptr(t, name, 0, device)
+
+
+def _product(fn, fmt, x, w, n, gated, y, slots, offsets, rows, stream):
+    fid, n = _fmt(fmt), int(n)
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+        raise ValueError("x must be a device matrix")
+    dt = DTYPES.get(x.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {x.dtype}")
+    tokens, k = x.shape
+    dev = x.get_device()
+    xp, ldx = _matrix(x, "x", k, dev)
+    experts = 1 if offsets is None else offsets.numel() - 1
+    if fid not in WEIGHT_FORMATS or n < 1 or k < 1 or experts < 1:
+        raise ValueError(f"no product of format {fmt!r} with n={n}, k={k}, {experts} expert(s)")
+    wp = _ptr(w, "w", _weight_bytes(fid, experts * n * (2 if gated else 1), k), dev)
+    if y is None:
+        y = _empty((slots, n), x.dtype, x.device, stream)
+    elif y.dim() != 2 or y.shape[0] != slots:
+        raise ValueError(f"y must have {slots} rows")
+    yp, ldy = _matrix(y, "y", n, dev, x.dtype)
+    if offsets is None:
+        st = _lib().qr_linear(fid, dt, bool(gated), xp, ldx, wp, yp, ldy, slots, n, k, _stream(stream, dev))
+    else:
+        op = _vector(offsets, "offsets", experts + 1, torch.int32, dev)
+        rp = None if rows is None else _vector(rows, "rows", slots, torch.int32, dev)
+        st = _lib().qr_experts(fid, dt, bool(gated), xp, ldx, tokens, wp, op, rp, yp, ldy, slots, experts, n, k,
+                               _stream(stream, dev))
+    _check(fn, st)
+    return y
+
+
+def qr_linear(fmt, x, w, n, gated=False, y=None, stream=None):
+    """``x`` [m, k] times the packed weight ``w`` [n, k] (``gated``: [2 n, k], the gate
+    rows and then the up rows, for silu(gate) * up); returns ``y`` [m, n]."""
+    return _product("qr_linear", fmt, x, w, n, gated, y, len(x), None, None, stream)
+
+
+def qr_experts(fmt, x, w, n, offsets, rows=None, gated=False, y=None, stream=None):
+    """The products of ``qr_linear`` with another weight for each group of rows.
+
+    ``w`` is the packed [experts, n, k] weight (``gated``: [experts, 2 n, k]).  Row s of
+    the result, for offsets[e] <= s < offsets[e + 1], is row ``rows[s]`` of ``x`` (row s
+    without ``rows``) times the weight of expert e; the rows from offsets[-1] on are zero."""
+    return _product("qr_experts", fmt, x, w, n, gated, y, len(x) if rows is None else rows.numel(), offsets, rows,
+                    stream)
+
+
+def qr_route(ids, experts, offsets=None, rows=None, pos=None, stream=None):
+    """Plan of the router's choice ``ids`` [tokens, top] (int32 or int64; a number outside
+    [0, experts) drops the slot): returns (offsets [experts + 1], rows [tokens * top],
+    pos [tokens, top]), all int32.  Rows offsets[e] to offsets[e + 1] of the sorted order
+    belong to expert e, sorted row s comes from token rows[s] (-1 past the last), and slot
+    (t, j) went to row pos[t, j] (-1: dropped)."""
+    if not (isinstance(ids, torch.Tensor) and ids.dim() == 2):
+        raise ValueError("ids must be a device matrix [tokens, top]")
+    idb = ID_TYPES.get(ids.dtype)
+    if idb is None:
+        raise ValueError(f"ids must be int32 or int64, not {ids.dtype}")
+    tokens, top = ids.shape
+    experts = int(experts)
+    ip = _ptr(ids, "ids", 0)
+    dev, slots = ids.get_device(), tokens * top
+    if experts < 1 or top < 1:
+        raise ValueError(f"no plan of {experts} expert(s), {top} a token")
+    if offsets is None:
+        offsets = _empty(experts + 1, torch.int32, ids.device, stream)
+    if rows is None:
+        rows = _empty(slots, torch.int32, ids.device, stream)
+    if pos is None:
+        pos = _empty((tokens, top), torch.int32, ids.device, stream)
+    op = _vector(offsets, "offsets", experts + 1, torch.int32, dev)
+    rp = _vector(rows, "rows", slots, torch.int32, dev)
+    pp = _vector(pos, "pos", slots, torch.int32, dev)
+    L = _lib()
+    nbytes = L.qr_route_workspace(tokens, top, experts)
+    ws = _empty(nbytes, torch.uint8, ids.device, stream) if nbytes else None  # scratch of this call
+    _check("qr_route", L.qr_route(ip, idb, op, rp, pp, tokens, top, experts, ws.data_ptr() if nbytes else None,
+                                  _stream(stream, dev)))
+    return offsets, rows, pos
+
+
+def qr_combine(y, pos, gates, out=None, stream=None):
+    """out[t] = sum over j of gates[t, j] * y[pos[t, j]] (a position outside y: no term);
+    ``pos`` int32 and ``gates`` fp32 are [tokens, top], ``y`` [slots, n]."""
+    if not (isinstance(y, torch.Tensor) and y.dim() == 2 and isinstance(pos, torch.Tensor) and pos.dim() == 2):
+        raise ValueError("y and pos must be device matrices")
+    dt = DTYPES.get(y.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {y.dtype}")
+    slots, n = y.shape
+    tokens, top = pos.shape
+    dev = y.get_device()
+    yp, ldy = _matrix(y, "y", n, dev)
+    if out is None:
+        out = _empty((tokens, n), y.dtype, y.device, stream)
+    elif out.dim() != 2 or out.shape[0] != tokens:
+        raise ValueError(f"out must have {tokens} rows")
+    op, ldo = _matrix(out, "out", n, dev, y.dtype)
+    pp = _vector(pos, "pos", tokens * top, torch.int32, dev)
+    gp = _vector(gates, "gates", tokens * top, torch.float32, dev)
+    _check("qr_combine", _lib().qr_combine(dt, yp, ldy, slots, pp, gp, op, ldo, tokens, top, n, _stream(stream, dev)))
+    return out

@@ -4,18 +4,43 @@
 
 namespace qr {
 
-template <int F, int DT, bool GATED>
-static qr_status launch_product(const ProductArgs& args, hipStream_t st) {
-  constexpr int MF = 1, NF = 1, WAVES = 8;
-  ProductArgs a = args;
-  a.ntiles = (a.n + 16 * NF - 1) / (16 * NF);
-  const long long groups = row_tiles(a.slots, a.experts, !a.offsets, 16 * MF) * a.ntiles;
-  if (groups > 0x7fffffffLL) return QR_ERR_SIZE;
+// Launches `kernel` for row tiles of `bm` rows and column tiles of `bc` columns of y.
+static qr_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs a, int bm, int bc, int threads, hipStream_t st) {
+  a.ntiles = (a.n + bc - 1) / bc;
+  const long long groups = row_tiles(a.slots, a.experts, !a.offsets, bm) * a.ntiles;
+  if (groups * threads > 0xffffffffLL) return QR_ERR_SIZE;  // a launch holds fewer than 2^32 threads
   void* argv[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(few_rows_kernel<F, DT, GATED, MF, NF, WAVES>),
-                         dim3((unsigned)groups), dim3(kWave * WAVES), argv, 0, st) == hipSuccess
+  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)groups), dim3(threads), argv, 0, st) ==
+                 hipSuccess
              ? QR_OK
              : QR_ERR_HIP;
+}
+
+template <int F, int DT, bool GATED, int NW, int KW>
+static qr_status launch_few(const ProductArgs& a, hipStream_t st) {
+  return launch_tiles(few_rows_kernel<F, DT, GATED, 1, NW, KW>, a, 16, 16 * NW / (GATED ? 2 : 1), kWave * NW * KW, st);
+}
+
+template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR>
+static qr_status launch_many(const ProductArgs& a, hipStream_t st) {
+  // rows of x that begin on 16 bytes go to LDS directly
+  const bool aligned = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0;
+  return launch_tiles(aligned ? many_rows_kernel<F, DT, GATED, WM, WN, MFR, NFR, true>
+                              : many_rows_kernel<F, DT, GATED, WM, WN, MFR, NFR, false>,
+                      a, 16 * WM * MFR, 16 * WN * NFR / (GATED ? 2 : 1), kWave * WM * WN, st);
+}
+
+template <int F, int DT, bool GATED>
+static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
+  const int rows = (int)((a.slots + (long long)a.experts - 1) / a.experts);  // of one expert, on average
+  if (rows <= 32) {
+    const long long quads = row_tiles(a.slots, a.experts, !a.offsets, 16) * ((a.n + 63) / 64) * (GATED ? 2 : 1);
+    if (quads >= 1024) return launch_few<F, DT, GATED, 8, 1>(a, st);
+    if (quads >= 192) return launch_few<F, DT, GATED, 4, 4>(a, st);
+    return launch_few<F, DT, GATED, GATED ? 2 : 1, GATED ? 4 : 8>(a, st);
+  }
+  if (rows <= 96) return launch_many<F, DT, GATED, 2, 2, 2, 4>(a, st);
+  return launch_many<F, DT, GATED, 2, 2, 4, 4>(a, st);
 }
 
 template <int F>

@@ -24,11 +24,10 @@ namespace qr {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-// 16- and 8-byte accesses at the alignment of a 2-byte value: rows of odd
+// 16-byte accesses at the alignment of a 2-byte value: rows of odd
 // stride are read and written without a special case (gfx950 serves unaligned
 // global accesses in hardware).
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
-typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 
 constexpr int kChunk = 128;        // values of k that one 16-byte load per lane covers
 constexpr int kChunkBlocks = kChunk / kBlockValues;
@@ -273,136 +272,548 @@ __device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 c) {
 // silu(g) * u in fp32.
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
-// Four neighbouring values of a row of y, columns c .. c + 3 of n.
-template <int DT>
-__device__ __forceinline__ void store4(uint8_t* row, int c, int n, const float (&v)[4]) {
-  const u32x2 p = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-  if (c + 4 <= n) {
-    *reinterpret_cast<u32x2_any*>(row + 2 * (size_t)c) = p;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (c + i < n) *reinterpret_cast<uint16_t*>(row + 2 * (size_t)(c + i)) = (uint16_t)(p[i >> 1] >> (16 * (i & 1)));
-  }
-}
-
 // ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
 
-// One workgroup computes 16 MF rows by 16 NF columns of y.  Its waves share
-// the k axis (wave w takes every WAVES-th chunk of 128), each weight block is
-// loaded and decoded once for all rows, and the waves' sums are joined through
-// LDS in the order of the waves.  Bound by reading the weights; x (16 MF rows)
-// comes from the caches.
-template <int F, int DT, bool GATED, int MF, int NF, int WAVES>
-__global__ __launch_bounds__(kWave * WAVES) void few_rows_kernel(ProductArgs a) {
+// A weight block as the few-row kernel multiplies it: the values without the
+// scale, exact in either dtype, and the scale applied to the fp32 sum over the
+// block.  One product of the matrix unit then has to cover one block (k = 32),
+// so the lanes (r, 0..3), which loaded blocks 0..3 of a chunk of row r whole,
+// exchange units: afterwards lane (r, g) holds unit g of block i in codes[i].
+// Four row swaps do it, two between the halves of the wave and two between
+// its odd and even rows of 16 lanes.
+__device__ __forceinline__ u32x4 exchange_units(u32x4 c) {
+  auto a = __builtin_amdgcn_permlane32_swap(c.x, c.z, false, false);
+  auto b = __builtin_amdgcn_permlane32_swap(c.y, c.w, false, false);
+  auto p = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  auto q = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{p[0], p[1], q[0], q[1]};
+}
+
+// The 8 values of a unit without the scale: E2M1 values; else the codes less
+// `zero` (SIGNED) or the codes themselves.
+template <int F, int DT, bool SIGNED>
+__device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
+  u32x4 o;
+  if constexpr (Format<F>::kFp4) {
+    if constexpr (DT == kFp16) {
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
+    } else {
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
+    }
+  } else {
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
+    const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+    // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
+    if constexpr (SIGNED) {
+      const f32x2 v01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.0f, false);
+      const f32x2 v23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.0f, true);
+      const f32x2 v45 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.0f, false);
+      const f32x2 v67 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.0f, true);
+      o.x = pack2<DT>(v01.x - zero, v01.y - zero);
+      o.y = pack2<DT>(v23.x - zero, v23.y - zero);
+      o.z = pack2<DT>(v45.x - zero, v45.y - zero);
+      o.w = pack2<DT>(v67.x - zero, v67.y - zero);
+    } else if constexpr (DT == kFp16) {
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f, false));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f, true));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f, false));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f, true));
+    } else {
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true));
+    }
+  }
+  return o;
+}
+
+// One workgroup multiplies 16 MF rows of x by NW fragments of 16 weight rows
+// (gated: NW / 2 of the gate rows and as many of the up rows).  Its KW x NW
+// waves share the k axis in KW groups (group kw takes every KW-th segment of
+// 512 values); a wave has one weight fragment, and the waves of a group share
+// the segment's x.  The groups' sums are joined through LDS in their order.
+//
+// Here x is the matrix unit's A and the weight its B, so that a lane's results
+// belong to the weight row whose blocks it loads: lane (r, g) has rows
+// 4 g .. 4 g + 3 of x and weight row r.  Of chunk c of a segment it loads block
+// 4 c + g; after exchange_units() product i of the chunk is block 4 c + i.
+//
+// Requests are dear: a load takes the CU's address unit a cycle for every
+// 64-byte piece it touches, 16 when four neighbouring lanes share one and 64
+// when each lane reads a row of its own, as the fragments of the matrix unit
+// want it.  The codes are loaded that way (a 16-byte piece lasts for four
+// products), x and the scales are not: lane 4 r + u loads them (unit u of row
+// r) and hands them to lane (r, g = u), x through LDS and the scales by a lane
+// permutation.
+//
+// sum_k x (c - z) is taken as sum_k x c - z sum_k x: the codes need no
+// subtraction, and sum_k x comes from one more product.  An infinity in x
+// would make that inf - inf; a wave whose sum is not finite computes it again
+// with the values c - z themselves.
+constexpr int kSegment = 512;
+constexpr int kSegBlocks = kSegment / kBlockValues;
+
+template <int F, int DT, int MF, int NW, int KW>
+struct FewRows {
+  static constexpr bool kAsym = Format<F>::kAsym;
+  static constexpr bool kZeros = !Format<F>::kFp4;  // codes have a zero point
+  static constexpr int XL = MF * kSegBlocks / NW;   // loads of x of one wave in a segment
+  static_assert(XL * NW == MF * kSegBlocks, "the waves of a group share the loads of x evenly");
+  // a wave that has x to itself writes it when it is done with the last segment;
+  // waves that share it write one copy while some still read the other
+  static constexpr int XB = NW == 1 ? 1 : 2;
+  union Stage {
+    u32x4 x[XB][KW][MF * kSegBlocks][16][4];  // [block][row][unit]
+    f32x4 sums[KW][NW][MF][kWave];            // ... and when x is done with, the waves' sums
+  };
+
+  const uint8_t* xrow[MF];  // row lane >> 2 of each fragment
+  bool here[MF];            // ... if there is one
+  const uint8_t* w;
+  uint32_t cblock;          // first block of weight row lane & 15, from w
+  uint32_t sblock;          // the same of row lane >> 2, whose scales this lane loads
+  f32x4 acc[MF];
+
+  struct Loads {
+    u32x4 codes[4];
+    uint32_t s[4];  // scales of blocks 4 u .. 4 u + 3, or their group's scale and zero point
+    u32x4 x[XL];
+  };
+
+  __device__ __forceinline__ void fetch(const ProductArgs& a, Loads& l, int seg, int nw, int lane) const {
+    constexpr uint32_t TB = Format<F>::kTileBytes;
+    const int last = a.blocks - 1, u = lane & 3, g = lane >> 4;
+    // a block past the row's last: that block again, times zeros of x
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int kb = seg * kSegBlocks + kChunkBlocks * c + g;
+      const uint32_t b = cblock + (uint32_t)(kb < last ? kb : last);
+      l.codes[c] = *reinterpret_cast<const u32x4*>(w + ((b >> 6) * TB + (b & 63) * 16));
+    }
+    const int kb = seg * kSegBlocks + kChunkBlocks * u;
+    if constexpr (kAsym) {
+      const uint32_t b = sblock + (uint32_t)(kb < last ? kb : last);
+      const uint32_t tile = (b >> 6) * TB, in = (b & 63) >> 2;
+      l.s[0] = *reinterpret_cast<const uint16_t*>(w + (tile + Format<F>::kScaleOffset + in * 2));
+      l.s[1] = w[tile + Format<F>::kZeroOffset + in];
+    } else if ((a.blocks & 3) == 0) {
+      // rows of whole groups of four: their scales are one aligned load
+      const uint32_t b = sblock + (uint32_t)(kb < last ? kb : last - 3);
+      const u32x2 v = *reinterpret_cast<const u32x2*>(w + ((b >> 6) * TB + Format<F>::kScaleOffset + (b & 63) * 2));
+      l.s[0] = v.x;
+      l.s[2] = v.y;
+      l.s[1] = l.s[3] = 0;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t b = sblock + (uint32_t)(kb + j < last ? kb + j : last);
+        l.s[j] = *reinterpret_cast<const uint16_t*>(w + ((b >> 6) * TB + Format<F>::kScaleOffset + (b & 63) * 2));
+      }
+    }
+    // unit u of some of the segment's blocks, of row lane >> 2
+    const int k0 = kSegment * seg + 8 * u;
+    const bool whole = kSegment * (seg + 1) <= a.k;
+#pragma unroll
+    for (int t = 0; t < XL; ++t) {
+      const int q = nw + NW * t, m = q / kSegBlocks, k = k0 + kBlockValues * (q % kSegBlocks);
+      l.x[t] = u32x4{0u, 0u, 0u, 0u};
+      if (m ? here[MF - 1] : here[0]) {
+        const uint8_t* row = m ? xrow[MF - 1] : xrow[0];
+        if (whole)
+          l.x[t] = *reinterpret_cast<const u32x4_any*>(row + 2 * (size_t)k);
+        else
+          l.x[t] = load_x8_tail(row, k, a.k);
+      }
+    }
+  }
+
+  // Adds this wave's share to acc.  All of the next segment loads while one is
+  // multiplied.
+  template <bool SIGNED>
+  __device__ __forceinline__ void sum(const ProductArgs& a, Stage& stage, int kw, int nw, int lane) {
+    const int r = lane & 15, g = lane >> 4;
+    const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int m = 0; m < MF; ++m) acc[m] = none;
+    // the factor of sum_k x: the zero point where it is the same for all
+    const uint32_t factor = kAsym ? (DT == kFp16 ? 0x3C003C00u : 0x3F803F80u)   // 1
+                                  : (DT == kFp16 ? 0xC800C800u : 0xC100C100u);  // -8
+    const u32x4 factors = {factor, factor, factor, factor};
+    const int segments = (a.blocks + kSegBlocks - 1) / kSegBlocks;
+    Loads l;
+    if (kw < segments) fetch(a, l, kw, nw, lane);
+    // every wave goes through as many rounds as the first group
+    for (int s0 = 0, buf = 0; s0 < segments; s0 += KW, buf ^= 1) {
+      const int seg = s0 + kw;
+      u32x4 codes[4], sc[2];
+      if (seg < segments) {
+#pragma unroll
+        for (int t = 0; t < XL; ++t) stage.x[buf % XB][kw][nw + NW * t][lane >> 2][(lane & 3) ^ (lane >> 4)] = l.x[t];
+#pragma unroll
+        for (int h = 0; h < (kAsym ? 1 : 2); ++h) {
+          // from lane 4 r + u to lane (r, u), and from row r's four lanes to each of them
+          const uint32_t s =
+              (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * r + g), (int)(l.s[2 * h] | l.s[2 * h + 1] << 16));
+          sc[h] = exchange_units(u32x4{s, s, s, s});
+        }
+#pragma unroll
+        for (int c = 0; c < 4; ++c) codes[c] = exchange_units(l.codes[c]);
+      }
+      if constexpr (NW == 1)
+        wave_lds_sync();
+      else
+        __syncthreads();
+      if (seg + KW < segments) fetch(a, l, seg + KW, nw, lane);
+      if (seg < segments) {
+        const u32x4(*xs)[16][4] = stage.x[buf % XB][kw];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          f32x4 part[MF], sx[MF];  // of the asymmetric format's group
+          const float z = kAsym ? (float)(sc[0][c] >> 16) : 8.0f;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const u32x4 wv = unit_values<F, DT, SIGNED>(codes[c][i], z);
+            const float d =
+                (float)__builtin_bit_cast(_Float16, (uint16_t)(kAsym ? sc[0][c] : sc[i >> 1][c] >> (16 * (i & 1))));
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+              const u32x4 x = xs[m * kSegBlocks + 4 * c + i][r][g ^ (r >> 2)];
+              if constexpr (kAsym && !SIGNED) {
+                part[m] = mfma<DT>(x, wv, i ? part[m] : none);
+                sx[m] = mfma<DT>(x, factors, i ? sx[m] : none);
+              } else {
+                f32x4 p = none;
+                if constexpr (kZeros && !SIGNED) p = mfma<DT>(x, factors, none);
+                p = mfma<DT>(x, wv, p);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) acc[m][t] = __builtin_fmaf(d, p[t], acc[m][t]);
+              }
+            }
+          }
+          if constexpr (kAsym && !SIGNED) {
+            const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)sc[0][c]);
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+                acc[m][t] = __builtin_fmaf(d, __builtin_fmaf(-z, sx[m][t], part[m][t]), acc[m][t]);
+          }
+        }
+      }
+    }
+  }
+};
+
+template <int F, int DT, bool GATED, int MF, int NW, int KW>
+__global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) {
+  using T = FewRows<F, DT, MF, NW, KW>;
   constexpr int HALVES = GATED ? 2 : 1;
-  constexpr int WF = NF * HALVES;  // weight fragments: NF of the gate rows (or all), NF of the up rows
-  __shared__ f32x4 sums[WAVES][MF * WF][kWave];
+  constexpr int NF = NW / HALVES;  // column fragments of y
+  __shared__ typename T::Stage stage;
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int kw = wave / NW, nw = wave % NW;
   const int r = lane & 15, g = lane >> 4;
   const int nt = blockIdx.x % a.ntiles;
   RowTile rt = find_rows<16 * MF>(a, blockIdx.x / a.ntiles);
   if (rt.m0 >= rt.m1) return;
-  rt.zero |= a.xrows == 0;  // every row number is out of range then, and no row of x can stand in
+  rt.zero |= a.xrows == 0;  // every row number is out of range then
   const int n0 = nt * 16 * NF;
 
-  const uint8_t* xrow[MF];
-  bool real[MF];
   if (!rt.zero) {
+    T t;
 #pragma unroll
-    for (int f = 0; f < MF; ++f) {
-      const int m = rt.m0 + 16 * f + r;
-      // rows past the end repeat the last one, which is in the caches
-      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
-      real[f] = s >= 0;
-      xrow[f] = a.x + 2 * (real[f] ? s : 0) * a.ldx;
+    for (int i = 0; i < MF; ++i) {
+      const int m = rt.m0 + 16 * i + (lane >> 2);
+      const long long s = m < rt.m1 ? source_row(a, m) : -1LL;
+      t.here[i] = s >= 0;
+      t.xrow[i] = a.x + 2 * (t.here[i] ? s : 0) * a.ldx;
     }
-    // the weight rows of this lane, as blocks from the tile that holds the
-    // first of them
-    const uint8_t* wbase[HALVES];
-    uint32_t wblock[WF];
+    const int c0 = n0 + 16 * (nw % NF);  // first weight row of the wave, of the gate or the up rows
+    const long long row0 = ((long long)rt.expert * HALVES + nw / NF) * a.n;
+    const long long first = (row0 + n0) * a.blocks;
+    t.w = a.w + (first >> 6) * Format<F>::kTileBytes;
+    // columns past the last repeat it
+    auto block_of = [&](int c) {
+      return (uint32_t)(first & 63) + (uint32_t)((c < a.n ? c : a.n - 1) - n0) * (uint32_t)a.blocks;
+    };
+    t.sblock = block_of(c0 + (lane >> 2));
+    t.cblock = block_of(c0 + r);
+    t.template sum<false>(a, stage, kw, nw, lane);
+    if constexpr (T::kZeros) {
+      bool finite = true;
 #pragma unroll
-    for (int h = 0; h < HALVES; ++h) {
-      const long long row0 = ((long long)rt.expert * HALVES + h) * a.n;
-      const long long first = (row0 + n0) * a.blocks;
-      wbase[h] = a.w + (first >> 6) * Format<F>::kTileBytes;
+      for (int i = 0; i < MF; ++i)
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        const int c = n0 + 16 * f + r;
-        wblock[h * NF + f] = (uint32_t)(first & 63) + (uint32_t)((c < a.n ? c : a.n - 1) - n0) * (uint32_t)a.blocks;
-      }
-    }
-    f32x4 acc[MF][WF];
+        for (int j = 0; j < 4; ++j) finite &= __builtin_fabsf(t.acc[i][j]) < __builtin_inff();
+      // the waves share x, so they decide together
+      if (__syncthreads_or(!finite)) {
+        f32x4 was[MF];
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-      for (int f = 0; f < WF; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
-    const int chunks = (a.blocks + kChunkBlocks - 1) / kChunkBlocks;
-    for (int c = wave; c < chunks; c += WAVES) {
-      const int kb = c * kChunkBlocks + g;
-      // past the row's last block: that block again, times zeros of x
-      const uint32_t b = (uint32_t)(kb < a.blocks ? kb : a.blocks - 1);
-      RawBlock raw[WF];
-#pragma unroll
-      for (int f = 0; f < WF; ++f) raw[f] = load_raw<F>(wbase[f / NF], wblock[f] + b);
-      u32x4 xv[MF][4];
-      const int k0 = kBlockValues * kb;
-      if (kChunk * (c + 1) <= a.k) {
+        for (int i = 0; i < MF; ++i) was[i] = t.acc[i];
+        t.template sum<true>(a, stage, kw, nw, lane);
+        // the finite ones stay as they are, so that no row depends on another
 #pragma unroll
         for (int i = 0; i < MF; ++i)
 #pragma unroll
-          for (int u = 0; u < 4; ++u) xv[i][u] = *reinterpret_cast<const u32x4_any*>(xrow[i] + 2 * (size_t)(k0 + 8 * u));
-      } else {
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int u = 0; u < 4; ++u) xv[i][u] = load_x8_tail(xrow[i], k0 + 8 * u, a.k);
-      }
-#pragma unroll
-      for (int f = 0; f < WF; ++f) {
-        const BlockScale<F, DT> s(raw[f]);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const u32x4 wv = decode_unit<F, DT>(raw[f].codes[u], s);
-#pragma unroll
-          for (int i = 0; i < MF; ++i) acc[i][f] = mfma<DT>(wv, xv[i][u], acc[i][f]);
-        }
+          for (int j = 0; j < 4; ++j)
+            if (__builtin_fabsf(was[i][j]) < __builtin_inff()) t.acc[i][j] = was[i][j];
       }
     }
+    __syncthreads();  // every wave is done with x
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-      for (int f = 0; f < WF; ++f) sums[wave][i * WF + f][lane] = acc[i][f];
-  } else {
-#pragma unroll
-    for (int f = 0; f < MF; ++f) real[f] = false;
+    for (int i = 0; i < MF; ++i) stage.sums[kw][nw][i][lane] = t.acc[i];
   }
   __syncthreads();
-  // fragment (i, f) of y is joined and stored by wave (i NF + f) % WAVES
+  // fragment (i, f) of y is joined and stored by wave i NF + f
+  if (wave >= MF * NF) return;
+  const int i = wave / NF, f = wave % NF;
+  f32x4 s[HALVES];
 #pragma unroll
-  for (int i = 0; i < MF; ++i)
+  for (int h = 0; h < HALVES; ++h) {
+    s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if (!rt.zero) {
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      if ((i * NF + f) % WAVES != wave) continue;
-      const int m = rt.m0 + 16 * i + r;
-      float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-      if (real[i]) {
-        f32x4 s[HALVES];
+      for (int k = 0; k < KW; ++k) s[h] += stage.sums[k][h * NF + f][i][lane];
+    }
+  }
+  const int c = n0 + 16 * f + r;
 #pragma unroll
-        for (int h = 0; h < HALVES; ++h) {
-          s[h] = sums[0][i * WF + h * NF + f][lane];
+  for (int j = 0; j < 4; ++j) {
+    const int m = rt.m0 + 16 * i + 4 * g + j;
+    const float v = GATED ? gate(s[0][j], s[HALVES - 1][j]) : s[0][j];
+    if (m < rt.m1 && c < a.n) *reinterpret_cast<uint16_t*>(a.y + 2 * (m * a.ldy + c)) = (uint16_t)pack2<DT>(v, 0.0f);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// many rows
+// ---------------------------------------------------------------------------
+
+// 16 bytes from each lane's address to lds + 16 lane, which is the same for the
+// whole wave.  In assembly, because the compiler would wait for it before the
+// next LDS read of any address, also of the buffer that is not being written;
+// it has no result that a register waits for.  M0 holds the LDS address; nothing
+// else here uses it.  Who reads the bytes waits with loads_done() and a barrier.
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, void* lds) {
+  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(p)
+               : "memory");
+}
+__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// A workgroup of WM x WN waves computes a tile of WM MFR 16 rows of x by WN NFR
+// 16 weight rows, each wave MFR x NFR fragments of it, in stages of 64 values
+// of k.  A stage's x and codes go to LDS without a stop in registers, the next
+// stage's while this one is multiplied; scales go through a register.  Each
+// wave decodes the weights it multiplies, rounded to the dtype as qr_decode
+// does, straight into the matrix unit's A: they pass LDS once, in 4 bits, and
+// the work of a decode is shared by MFR products.
+//
+// LDS: row m of x is 8 units of 16 bytes, unit u at place u ^ (m & 7), so that
+// 8 lanes that read one unit of 8 rows hit 8 groups of banks; the lanes that
+// load it take their units in that order.
+//
+// A lane's results are 4 neighbouring weight rows of one row of x.  Fragments
+// come in pairs whose rows interleave by fours, so that it has 8 neighbours:
+// one 16-byte store.  Gated: the first half of a wave's fragments are gate
+// rows, the second the same columns' up rows.
+constexpr int kStage = 64;
+constexpr int kStageBlocks = kStage / kBlockValues;
+
+// Tile of the launch's index space that workgroup `id` of `total` computes.
+// Workgroups are dealt to the 8 XCDs in turn; each XCD takes a contiguous run
+// of tiles, ordered in bands of kBand row tiles by all column tiles, so that
+// the tiles that run on it at one time share rows of x and of the weight in
+// its L2.
+constexpr int kBand = 4;
+struct TileIndex {
+  int row, col;
+};
+__device__ __forceinline__ TileIndex tile_index(int id, int total, int ncols) {
+  const int per = total / 8, rest = total % 8, xcd = id % 8;
+  const int t = xcd * per + (xcd < rest ? xcd : rest) + id / 8;
+  const int rows = total / ncols, band = t / (kBand * ncols), in = t - band * kBand * ncols;
+  const int height = rows - band * kBand < kBand ? rows - band * kBand : kBand;
+  return {band * kBand + in % height, in / height};
+}
+
+template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR, bool ALIGNED>
+__global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs a) {
+  static_assert(NFR % (GATED ? 4 : 2) == 0, "fragments come in pairs");
+  constexpr int WAVES = WM * WN, HALVES = GATED ? 2 : 1;
+  constexpr int BM = 16 * WM * MFR, BN = 16 * WN * NFR;
+  constexpr int COLS = 16 * NFR / HALVES;         // columns of y of one wave
+  constexpr int XI = BM / 8 / WAVES;              // loads of x of one wave in a stage: 8 rows each
+  constexpr int WI = BN / 32;                     // loads of codes of the workgroup: 32 rows each
+  static_assert(XI * 8 * WAVES == BM, "the waves share the loads of x evenly");
+  static_assert(WI <= WAVES, "at most one load of codes for each wave");
+  constexpr uint32_t TB = Format<F>::kTileBytes;
+  constexpr bool kAsym = Format<F>::kAsym;
+  struct Buffer {
+    u32x4 x[BM][8];
+    u32x4 codes[BN][kStageBlocks];
+    uint32_t scales[BN];  // of both blocks, or the group's scale and zero point
+  };
+  __shared__ Buffer lds[2];
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r = lane & 15, g = lane >> 4;
+  const TileIndex ti = tile_index(blockIdx.x, gridDim.x, a.ntiles);
+  RowTile rt = find_rows<BM>(a, ti.row);
+  if (rt.m0 >= rt.m1) return;
+  rt.zero |= a.xrows == 0;  // every row number is out of range then
+  const int n0 = ti.col * (BN / HALVES);
+
+  f32x4 acc[MFR][NFR];
 #pragma unroll
-          for (int w = 1; w < WAVES; ++w) s[h] += sums[w][i * WF + h * NF + f][lane];
+  for (int i = 0; i < MFR; ++i)
+#pragma unroll
+    for (int f = 0; f < NFR; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+  if (!rt.zero) {
+    // x: load i of this wave brings rows 8 (XI wave + i) + lane / 8 of the tile,
+    // unit (lane & 7) ^ (row & 7); rows past the end repeat the last, rows of no
+    // source the first of x
+    const uint8_t* xrow[XI];
+    const int unit = (lane & 7) ^ (lane >> 3);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const int m = rt.m0 + 8 * (XI * wave + i) + (lane >> 3);
+      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
+      xrow[i] = a.x + 2 * (s < 0 ? 0 : s) * a.ldx + 16 * unit;
+    }
+    // weights: row R of the tile is column col(R) of its half; columns past the last repeat it
+    const long long row0 = (long long)rt.expert * HALVES * a.n;
+    const long long first = (row0 + n0) * a.blocks;
+    const uint8_t* wb = a.w + (first >> 6) * TB;
+    const int R = 32 * wave + (lane >> 1);  // this lane's row, if wave < WI
+    long long wrow = 0;
+    {
+      const int f = R / 16 % NFR, q = R & 15;
+      const int half = GATED ? f / (NFR / 2) : 0, ff = GATED ? f % (NFR / 2) : f;
+      const int c = n0 + COLS * (R / (16 * NFR)) + 32 * (ff >> 1) + 8 * (q >> 2) + 4 * (ff & 1) + (q & 3);
+      wrow = (long long)half * a.n + (c < a.n ? c : a.n - 1) - n0;
+    }
+    // its first block, from wb: up rows are n rows further, past 32 bits of bytes
+    const long long wblock = (first & 63) + wrow * a.blocks;
+    const uint8_t* wlane = wb + (wblock >> 6) * TB;
+    const uint32_t wfirst = (uint32_t)(wblock & 63);
+
+    const int last = a.blocks - 1;
+    const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
+    uint32_t sv[2] = {0u, 0u};
+    u32x4 xv[XI];
+    // stages whose x cannot go to LDS directly: rows that are not 16-byte
+    // aligned, and the last values of a row
+    auto through_registers = [&](int st) { return !ALIGNED || kStage * (st + 1) > a.k; };
+    auto fetch = [&](int st, Buffer& to) {
+      if (wave < WI) {
+        const int kb = st * kStageBlocks + (lane & 1);
+        const uint32_t b = wfirst + (uint32_t)(kb < last ? kb : last);  // past the last: that one, times zeros of x
+        const uint32_t at = (b >> 6) * TB, in = b & 63;
+        load_to_lds(wlane + (at + in * 16), &to.codes[32 * wave][0]);
+        if constexpr (kAsym) {
+          // both lanes of a row load the same
+          sv[0] = *reinterpret_cast<const uint16_t*>(wlane + (at + Format<F>::kScaleOffset + (in >> 2) * 2));
+          sv[1] = wlane[at + Format<F>::kZeroOffset + (in >> 2)];
+        } else {
+          sv[0] = *reinterpret_cast<const uint16_t*>(wlane + (at + Format<F>::kScaleOffset + in * 2));
+        }
+      }
+      if (through_registers(st)) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i) xv[i] = load_x8_tail(xrow[i] - 16 * unit, kStage * st + 8 * unit, a.k);
+      } else {
+#pragma unroll
+        for (int i = 0; i < XI; ++i)
+          load_to_lds(xrow[i] + 2 * kStage * (size_t)st, &to.x[8 * (XI * wave + i)][0]);
+      }
+    };
+    fetch(0, lds[0]);
+    for (int st = 0; st < stages; ++st) {
+      Buffer& now = lds[st & 1];
+      loads_done();
+      if (wave < WI) {
+        if constexpr (kAsym) {
+          now.scales[R] = sv[0] | sv[1] << 16;
+        } else {
+          reinterpret_cast<uint16_t*>(&now.scales[R])[lane & 1] = (uint16_t)sv[0];
+        }
+      }
+      if (through_registers(st)) {
+#pragma unroll
+        for (int i = 0; i < XI; ++i) now.x[8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
+      }
+      __syncthreads();
+      if (st + 1 < stages) fetch(st + 1, lds[(st + 1) & 1]);
+
+      uint32_t scale[NFR];
+#pragma unroll
+      for (int f = 0; f < NFR; ++f) scale[f] = now.scales[16 * (NFR * wn + f) + r];
+#pragma unroll
+      for (int b = 0; b < kStageBlocks; ++b) {
+        u32x4 wv[NFR];
+#pragma unroll
+        for (int f = 0; f < NFR; ++f) {
+          RawBlock raw;
+          raw.scale = kAsym ? scale[f] & 0xffffu : (scale[f] >> (16 * b)) & 0xffffu;
+          raw.zero = kAsym ? scale[f] >> 16 : 0u;
+          const BlockScale<F, DT> s(raw);
+          const uint32_t code = reinterpret_cast<const uint32_t*>(&now.codes[16 * (NFR * wn + f) + r][b])[g];
+          wv[f] = decode_unit<F, DT>(code, s);
         }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) v[j] = GATED ? gate(s[0][j], s[HALVES - 1][j]) : s[0][j];
+        for (int i = 0; i < MFR; ++i) {
+          const u32x4 x = now.x[16 * (MFR * wm + i) + r][(4 * b + g) ^ (r & 7)];
+#pragma unroll
+          for (int f = 0; f < NFR; ++f) acc[i][f] = mfma<DT>(wv[f], x, acc[i][f]);
+        }
       }
-      if (m < rt.m1) store4<DT>(a.y + 2 * (long long)m * a.ldy, n0 + 16 * f + 4 * g, a.n, v);
     }
+  }
+
+#pragma unroll
+  for (int i = 0; i < MFR; ++i) {
+    const int m = rt.m0 + 16 * (MFR * wm + i) + r;
+    if (m >= rt.m1) continue;
+    const bool real = !rt.zero && source_row(a, m) >= 0;
+    uint8_t* row = a.y + 2 * (long long)m * a.ldy;
+#pragma unroll
+    for (int p = 0; p < NFR / HALVES; p += 2) {
+      float v[8];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float h = acc[i][p + e][j];
+          v[4 * e + j] = !real ? 0.0f : GATED ? gate(h, acc[i][p + e + (GATED ? NFR / 2 : 0)][j]) : h;
+        }
+      const int c = n0 + COLS * wn + 16 * p + 8 * g;
+      const u32x4 o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+      if (c + 8 <= a.n) {
+        *reinterpret_cast<u32x4_any*>(row + 2 * (size_t)c) = o;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (c + j < a.n)
+            *reinterpret_cast<uint16_t*>(row + 2 * (size_t)(c + j)) = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------

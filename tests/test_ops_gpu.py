@@ -1,11 +1,13 @@
 """The operators over 4-bit weights against plain computations in 64 bits (MI355X only).
 
-Tolerances follow from the operators' definitions.  A product's weights are the
-packed ones rounded to the call's dtype, which the reference does too; what
-remains is the fp32 sum of k exact products (k 2^-23 of the sum of their
-magnitudes, which also covers truncating adders), and one rounding of the
-result (2^-11 of it for fp16, 2^-8 for bf16, half the smallest subnormal below
-the normal range).  silu(g) * u passes the errors of g and u on with the
+Tolerances follow from the operators' definitions.  A product multiplies by the
+weights code value times scale, and with many rows by these rounded to the
+call's dtype; it has to agree with one or the other throughout.  What remains
+is the fp32 sum of k products (k 2^-23 of the sum of their magnitudes, which
+also covers truncating adders; a format with a zero point may sum codes and
+zero points apart, whose magnitudes are up to 15 and 15 steps), and one rounding
+of the result (2^-11 of it for fp16, 2^-8 for bf16, half the smallest subnormal
+below the normal range).  silu(g) * u passes the errors of g and u on with the
 magnitudes of its derivatives, |silu'| <= 1.1, and adds its own evaluation
 (|g| + 8 units of 2^-23).
 """
@@ -52,7 +54,8 @@ def random_packed(fmt, rows, k, seed, scale=0.05):
 
 
 def weight64(fmt, packed, rows, k, dtype):
-    """[rows, k] weight of packed tiles, rounded to the dtype, in fp64."""
+    """[rows, k] weight of packed tiles in fp64: rounded to the dtype, exact, and
+    the magnitudes that the codes and the zero points have summed apart."""
     kp = -(-k // GROUP[fmt]) * GROUP[fmt]
     code = np.stack([packed[:, :1024] & 15, packed[:, :1024] >> 4], 2).reshape(-1, 2048)
     groups = 2048 // GROUP[fmt]
@@ -63,17 +66,29 @@ def weight64(fmt, packed, rows, k, dtype):
         v = code.astype(np.float64) - 8
     else:
         v = code.astype(np.float64) - np.repeat(packed[:, 1056:].astype(np.float64), 128, 1)
-    w = (v * np.repeat(s, GROUP[fmt], 1)).reshape(-1)[:rows * kp].reshape(rows, kp)[:, :k]
+    def matrix(v):
+        return (v * np.repeat(s, GROUP[fmt], 1)).reshape(-1)[:rows * kp].reshape(rows, kp)[:, :k]
+
+    w = matrix(v)
     # value * scale has at most 15 significant bits: exact in fp32
-    return torch.from_numpy(w.astype(np.float32)).to(DT[dtype]).double().numpy()
+    rounded = torch.from_numpy(w.astype(np.float32)).to(DT[dtype]).double().numpy()
+    return rounded, w, np.abs(w) if fmt == "fp4" else matrix(code + (code - v))
 
 
-def check_product(got, x, w, n, gated, dtype, what):
-    """got, x: device tensors; w: fp64 numpy weight."""
+def check_product(got, x, weights, n, gated, dtype, what):
+    """got, x: device tensors; weights: what weight64() gives, of the rows in question."""
     x64, y = x.double().cpu().numpy(), got.double().cpu().numpy()
+    rounded, exact, apart = weights
+    found = [wrong(y, x64, w, mag, n, gated, dtype) for w, mag in ((rounded, np.abs(rounded)), (exact, apart))]
+    assert any(not bad.any() for bad, _ in found), (what, [(np.argwhere(bad)[:4].tolist(), y[bad][:4], want[bad][:4],
+                                                            int(bad.sum())) for bad, want in found])
+
+
+def wrong(y, x64, w, mag, n, gated, dtype):
+    """Which values of y are not silu(x w') etc. within the tolerance, and what is right."""
     k = x64.shape[1]
-    h, mag = x64 @ w.T, np.abs(x64) @ np.abs(w).T
-    err = k * 2.0 ** -23 * mag
+    h = x64 @ w.T
+    err = k * 2.0 ** -23 * (np.abs(x64) @ mag.T)
     if gated:
         g, u, eg, eu = h[:, :n], h[:, n:], err[:, :n], err[:, n:]
         silu = g / (1 + np.exp(-np.clip(g, -700, 700)))
@@ -82,8 +97,7 @@ def check_product(got, x, w, n, gated, dtype, what):
     else:
         want = h
     tol = err + HALF_ULP[dtype] * (np.abs(want) + err) + TINY[dtype]
-    bad = ~(np.abs(y - want) <= tol)
-    assert not bad.any(), (what, np.argwhere(bad)[:4].tolist(), y[bad][:4], want[bad][:4], int(bad.sum()))
+    return ~(np.abs(y - want) <= tol), want
 
 
 def activations(m, k, dtype, seed):
@@ -151,7 +165,7 @@ def test_extreme_scales(qa, fmt, dtype, m):
     """Each value of W alone (one-hot rows of x): exact for every scale that leaves it finite."""
     n, k = 48, 384
     p = extreme_scales(fmt, n, k, 11)
-    w = weight64(fmt, p, n, k, dtype)
+    w = weight64(fmt, p, n, k, dtype)[0]
     cols = np.random.default_rng(5).integers(0, k, m)
     x = torch.zeros(m, k, dtype=DT[dtype])
     x[np.arange(m), cols] = 1
@@ -216,7 +230,7 @@ def check_experts(qa, fmt, dtype, gated, sizes, n, k, tail, gather, seed):
         lo, hi = offsets[e], offsets[e + 1]
         if hi > lo:
             xe = x[torch.from_numpy(rows[lo:hi]).long().cuda()] if gather else x[lo:hi]
-            check_product(y[lo:hi], xe, w[e * wide:(e + 1) * wide], n, gated, dtype, (fmt, dtype, gated, e, n, k))
+            check_product(y[lo:hi], xe, [v[e * wide:(e + 1) * wide] for v in w], n, gated, dtype, (fmt, dtype, gated, e, n, k))
     assert (y[offsets[-1]:] == 0).all()
 
 

@@ -16,6 +16,25 @@ static qr_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs a, int bm
              : QR_ERR_HIP;
 }
 
+template <int F, int DT, bool GATED, int MR, int KS>
+static qr_status launch_row(const ProductArgs& a, hipStream_t st) {
+  return launch_tiles(row_kernel<F, DT, GATED, MR, KS>, a, MR, kRowWaves / KS * kRowsPerWave / (GATED ? 2 : 1),
+                      kWave * kRowWaves, st);
+}
+
+template <int F, int DT, bool GATED, int MR>
+static qr_status launch_rows(const ProductArgs& a, hipStream_t st) {
+  // Several waves share the k axis where there is more than a slice of it for
+  // each, and where the workgroups would not fill the CUs otherwise: 4096 rows
+  // of weights of k = 4096, 128 workgroups 6.4 us, 256 with two waves each 6.0;
+  // 16384 rows of 8192, 512 workgroups 17.1 us, 2048 with four waves each 21.9.
+  const long long groups = row_tiles(a.slots, a.experts, !a.offsets, MR) * a.n * (GATED ? 2 : 1) /
+                           (kRowWaves * kRowsPerWave);  // of KS = 1
+  if (a.blocks <= kWave || groups >= 256) return launch_row<F, DT, GATED, MR, 1>(a, st);
+  if (a.blocks <= 2 * kWave || groups >= 128) return launch_row<F, DT, GATED, MR, 2>(a, st);
+  return launch_row<F, DT, GATED, MR, 4>(a, st);
+}
+
 template <int F, int DT, bool GATED, int NW, int KW>
 static qr_status launch_few(const ProductArgs& a, hipStream_t st) {
   return launch_tiles(few_rows_kernel<F, DT, GATED, 1, NW, KW>, a, 16, 16 * NW / (GATED ? 2 : 1), kWave * NW * KW, st);
@@ -33,6 +52,10 @@ static qr_status launch_many(const ProductArgs& a, hipStream_t st) {
 template <int F, int DT, bool GATED>
 static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   const int rows = (int)((a.slots + (long long)a.experts - 1) / a.experts);  // of one expert, on average
+  // groups of unknown sizes: few rows in all
+  const int most = a.offsets ? a.slots / 4 : a.slots;
+  if (most <= 1) return launch_rows<F, DT, GATED, 1>(a, st);
+  if (most <= 2) return launch_rows<F, DT, GATED, 2>(a, st);
   if (rows <= 32) {
     const long long quads = row_tiles(a.slots, a.experts, !a.offsets, 16) * ((a.n + 63) / 64) * (GATED ? 2 : 1);
     if (quads >= 1024) return launch_few<F, DT, GATED, 8, 1>(a, st);

@@ -16,6 +16,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "qr.h"
 #include "qr_codec.hpp"
 
@@ -110,12 +112,13 @@ __device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t) {
   return rt;
 }
 
-// Largest number of row tiles that find_rows() can hand out: every group ends
-// in at most one partial tile, and no more groups than rows are not empty.
+// Largest number of row tiles that find_rows() can hand out: no more groups
+// than rows are not empty, each has a tile that holds at least one row, and the
+// other tiles are full.
 inline long long row_tiles(long long slots, long long experts, bool dense, int bm) {
   if (dense) return (slots + bm - 1) / bm;
   const long long groups = experts + 1 < slots ? experts + 1 : slots;
-  return slots / bm + groups;
+  return groups + (slots - groups) / bm;
 }
 
 // Row of x that row m of y is computed from, -1 if none.
@@ -244,18 +247,26 @@ __device__ __forceinline__ u32x4 decode_unit(uint32_t w, const BlockScale<F, DT>
 // x: 8 values of a row
 // ---------------------------------------------------------------------------
 
-// Values k0 .. k0 + 7 of a row; those from k on are zero and are not read.
+// Values k0 .. k0 + 7 of a row of k; those from k on are zero and are not read.
+// No branch but one that is the same for the whole launch, so that several such
+// loads are in flight together: the last 8 values of the row are moved down.
 __device__ __forceinline__ u32x4 load_x8_tail(const uint8_t* row, int k0, int k) {
+  typedef unsigned long long u64x2 __attribute__((ext_vector_type(2)));
+  if (k >= 8) {
+    const int from = k0 < k - 8 ? k0 : k - 8;
+    const u64x2 v = __builtin_bit_cast(u64x2, *reinterpret_cast<const u32x4_any*>(row + 2 * (size_t)from));
+    const int drop = k0 - from < 8 ? k0 - from : 8;  // values
+    const int low = 16 * (drop & 3);
+    const unsigned long long down = low ? v.x >> low | v.y << (64 - low) : v.x;
+    const unsigned long long high = v.y >> low;
+    return __builtin_bit_cast(u32x4, drop >= 8 ? u64x2{0, 0} : drop >= 4 ? u64x2{high, 0} : u64x2{down, high});
+  }
   u32x4 v = {0u, 0u, 0u, 0u};
-  if (k0 + 8 <= k) {
-    v = *reinterpret_cast<const u32x4_any*>(row + 2 * (size_t)k0);
-  } else {
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (k0 + j < k) {
-        const uint32_t h = *reinterpret_cast<const uint16_t*>(row + 2 * ((size_t)k0 + j));
-        v[j >> 1] |= (j & 1) ? h << 16 : h;
-      }
+  for (int j = 0; j < 7; ++j) {
+    const int at = k0 + j < k ? k0 + j : k - 1;
+    const uint32_t h = *reinterpret_cast<const uint16_t*>(row + 2 * (size_t)at);
+    if (k0 + j < k) v[j >> 1] |= (j & 1) ? h << 16 : h;
   }
   return v;
 }
@@ -271,6 +282,180 @@ __device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 c) {
 
 // silu(g) * u in fp32.
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
+
+// ---------------------------------------------------------------------------
+// one or two rows
+// ---------------------------------------------------------------------------
+
+// The 8 values of a unit in fp32, without the scale.
+template <int F>
+__device__ __forceinline__ void unit_f32(uint32_t w, float zero, float (&v)[8]) {
+  if constexpr (Format<F>::kFp4) {
+    const f32x2 a = fp4_unpack<0>(w), b = fp4_unpack<1>(w), c = fp4_unpack<2>(w), d = fp4_unpack<3>(w);
+    v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y; v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
+  } else if constexpr (Format<F>::kAsym) {
+    // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
+    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.0f, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.0f, true);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.0f, false);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.0f, true);
+    v[0] = a.x - zero; v[2] = a.y - zero; v[4] = b.x - zero; v[6] = b.y - zero;
+    v[1] = c.x - zero; v[3] = c.y - zero; v[5] = d.x - zero; v[7] = d.y - zero;
+  } else {
+    // signed bytes 16 (c - 8); the 16 is taken out of the scale
+    const uint32_t lo = ((w << 4) & 0xF0F0F0F0u) ^ 0x80808080u, hi = (w & 0xF0F0F0F0u) ^ 0x80808080u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = sbyte(lo, i);
+      v[2 * i + 1] = sbyte(hi, i);
+    }
+  }
+}
+
+// The sum over the wave's lanes, in lane 63: within each row of 16 lanes, and
+// then from row to row.
+__device__ __forceinline__ float wave_sum(float v) {
+  auto add = [&](auto ctrl) {
+    v += __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, v), decltype(ctrl)::value, 0xF,
+                                                               0xF, true));
+  };
+  add(std::integral_constant<int, 0x111>{});  // row_shr:1
+  add(std::integral_constant<int, 0x112>{});  // row_shr:2
+  add(std::integral_constant<int, 0x114>{});  // row_shr:4
+  add(std::integral_constant<int, 0x118>{});  // row_shr:8
+  add(std::integral_constant<int, 0x142>{});  // row_bcast:15
+  add(std::integral_constant<int, 0x143>{});  // row_bcast:31
+  return v;
+}
+
+// One workgroup multiplies MR rows of x by kRowsPerWave weight rows for each of
+// its 8 / KS groups of KS waves; the waves of a group share the k axis in
+// slices of 2048 values, one 32-value block a lane, so that a row's codes and
+// scales are read in whole lines.  x goes through LDS once for the workgroup
+// and stays in fp32 registers for the wave's weight rows; every product and
+// sum is an fp32 FMA.  Bound by reading the weights, and in small calls by the
+// one trip to memory: all of a slice's loads are in flight at once.
+constexpr int kRowWaves = 8;
+constexpr int kRowsPerWave = 4;
+constexpr int kSlice = kWave * kBlockValues;
+
+template <int F, int DT, bool GATED, int MR, int KS>
+__global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
+  constexpr int HALVES = GATED ? 2 : 1, R = kRowsPerWave, GROUPS = kRowWaves / KS;
+  constexpr int CW = R / HALVES, COLS = GROUPS * CW;  // columns of y of a wave, of the workgroup
+  constexpr int XC = MR * KS * kSlice / 8;            // 16-byte pieces of x in a panel of KS slices
+  __shared__ u32x4 lds_x[XC];
+  __shared__ float sums[kRowWaves][MR][R];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int ks = wave % KS, c0 = (blockIdx.x % a.ntiles) * COLS;
+  RowTile rt = find_rows<MR>(a, blockIdx.x / a.ntiles);
+  if (rt.m0 >= rt.m1) return;
+  rt.zero |= a.xrows == 0;  // every row number is out of range then
+  long long src[MR];
+#pragma unroll
+  for (int m = 0; m < MR; ++m) src[m] = rt.zero || rt.m0 + m >= rt.m1 ? -1 : source_row(a, rt.m0 + m);
+
+  // weight rows as blocks from the tile that holds the workgroup's first of each half
+  const uint8_t* w[HALVES];
+  uint32_t first[R];
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h) {
+    const long long b = (((long long)(rt.zero ? 0 : rt.expert) * HALVES + h) * a.n + c0) * a.blocks;
+    w[h] = a.w + (b >> 6) * Format<F>::kTileBytes;
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+      const int c = c0 + (wave / KS) * CW + i;  // columns past the last repeat it
+      first[h * CW + i] = (uint32_t)(b & 63) + (uint32_t)((c < a.n ? c : a.n - 1) - c0) * (uint32_t)a.blocks;
+    }
+  }
+  float acc[MR][R];
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int i = 0; i < R; ++i) acc[m][i] = 0.0f;
+  const int panels = rt.zero ? 0 : (a.blocks + KS * kWave - 1) / (KS * kWave);
+  for (int p = 0; p < panels; ++p) {
+    const int kb = (p * KS + ks) * kWave + lane;
+    // past the row's last block: that block again, times zeros of x
+    const uint32_t b = (uint32_t)(kb < a.blocks ? kb : a.blocks - 1);
+    RawBlock raw[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) raw[i] = load_raw<F>(w[i / CW], first[i] + b);
+    u32x4 xv[(XC + kWave * kRowWaves - 1) / (kWave * kRowWaves)];
+    const int k0 = p * KS * kSlice;
+#pragma unroll
+    for (int t = 0; t < (int)(sizeof(xv) / sizeof(xv[0])); ++t) {
+      const int q = tid + kWave * kRowWaves * t, m = MR == 1 ? 0 : q / (XC / MR), k = k0 + 8 * (q % (XC / MR));
+      xv[t] = u32x4{0u, 0u, 0u, 0u};
+      const long long s = MR > 1 && m ? src[MR - 1] : src[0];
+      if (q < XC && s >= 0 && k < a.k) xv[t] = load_x8_tail(a.x + 2 * s * a.ldx, k, a.k);
+    }
+    if (p) __syncthreads();  // everyone is done with the last panel's x
+    // lane l reads pieces 4 l .. 4 l + 3, which lie at places (piece ^ l / 4) of its 64 bytes:
+    // 8 lanes that read one of them hit 8 groups of banks
+#pragma unroll
+    for (int t = 0; t < (int)(sizeof(xv) / sizeof(xv[0])); ++t) {
+      const int q = tid + kWave * kRowWaves * t;
+      if (q < XC) lds_x[q ^ ((q >> 4) & 3)] = xv[t];
+    }
+    __syncthreads();
+    float x[MR][kBlockValues];
+#pragma unroll
+    for (int m = 0; m < MR; ++m)
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int q = (m * KS + ks) * (kSlice / 8) + 4 * lane + u;
+        const u32x4 v = lds_x[q ^ ((q >> 4) & 3)];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[m][8 * u + 2 * i] = lo_to_f32<DT>(v[i]);
+          x[m][8 * u + 2 * i + 1] = hi_to_f32<DT>(v[i]);
+        }
+      }
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      float t[MR][2];
+#pragma unroll
+      for (int m = 0; m < MR; ++m) t[m][0] = t[m][1] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        float v[8];
+        unit_f32<F>(raw[i].codes[u], (float)raw[i].zero, v);
+#pragma unroll
+        for (int m = 0; m < MR; ++m)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[m][j & 1] = __builtin_fmaf(v[j], x[m][8 * u + j], t[m][j & 1]);
+      }
+      float d = (float)__builtin_bit_cast(_Float16, (uint16_t)raw[i].scale);
+      if constexpr (!Format<F>::kAsym && !Format<F>::kFp4) d *= 0.0625f;
+#pragma unroll
+      for (int m = 0; m < MR; ++m) acc[m][i] = __builtin_fmaf(d, t[m][0] + t[m][1], acc[m][i]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MR; ++m)
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const float v = wave_sum(acc[m][i]);
+      if (lane == kWave - 1) sums[wave][m][i] = v;
+    }
+  __syncthreads();
+  if (tid >= MR * COLS) return;
+  const int m = tid / COLS, col = tid % COLS, grp = col / CW;
+  if (rt.m0 + m >= rt.m1 || c0 + col >= a.n) return;
+  float s[HALVES];
+#pragma unroll
+  for (int h = 0; h < HALVES; ++h) {
+    s[h] = sums[grp * KS][m][h * CW + col % CW];
+#pragma unroll
+    for (int k = 1; k < KS; ++k) s[h] += sums[grp * KS + k][m][h * CW + col % CW];
+  }
+  const float v = GATED ? gate(s[0], s[HALVES - 1]) : s[0];
+  const bool real = MR > 1 && m ? src[MR - 1] >= 0 : src[0] >= 0;
+  *reinterpret_cast<uint16_t*>(a.y + 2 * ((rt.m0 + m) * a.ldy + c0 + col)) = (uint16_t)pack2<DT>(real ? v : 0.0f, 0.0f);
+}
 
 // ---------------------------------------------------------------------------
 // few rows

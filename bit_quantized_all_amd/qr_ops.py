@@ -75,33 +75,33 @@ def qr_encode_weight(fmt, w, packed=None, stream=None):
     else:
         flat = w.contiguous().view(-1)
     if packed is None:
-        packed = _empty(nbytes, torch.uint8, w.device, stream)
+        packed = _empty(w, (nbytes,), torch.uint8, stream)
     qr_encode(fid, flat, packed, stream)
     return packed
 
 
-def _empty(shape, dtype, device, stream):
-    """A new tensor of the stream that will write it: the caching allocator hands
-    memory on in the order of the stream that was current when it was taken."""
+def _empty(like, shape, dtype, stream):
+    """A new tensor on the device of ``like``, of the stream that will write it: the
+    caching allocator hands memory on in the order of the stream that was current
+    when it was taken."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
+        return like.new_empty(shape, dtype=dtype)
 
 
-def _matrix(t, name, cols, device, dtype=None):
+def _matrix(t, name, rows, cols, device, dtype):
     """Address and row stride of a device matrix of ``cols`` neighbouring values a row."""
     if not (isinstance(t, torch.Tensor) and t.is_cuda and t.dim() == 2):
         raise ValueError(f"{name} must be a device matrix")
     if t.get_device() != device:
         raise ValueError(f"{name} is on device {t.get_device()}, the call's tensors are on device {device}")
-    if dtype is not None and t.dtype != dtype:
+    if t.dtype != dtype:
         raise ValueError(f"{name} is {t.dtype}, the call's dtype is {dtype}")
-    rows, have = t.shape
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {(rows, cols)}")
     ld, step = t.stride()
-    if have != cols:
-        raise ValueError(f"{name} has {have} columns, the call needs {cols}")
-    if have > 1 and step != 1:
+    if step != 1 and cols > 1:
         raise ValueError(f"the values of a row of {name} must be neighbours")
     if rows < 2:
         ld = cols
@@ -118,40 +118,51 @@ def _vector(t, name, numel, dtype, device):
     return _ptr(t, name, 0, device)
 
 
-def _product(fn, fmt, x, w, n, gated, y, slots, offsets, rows, stream):
-    fid, n = _fmt(fmt), int(n)
-    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
-        raise ValueError("x must be a device matrix")
-    dt = DTYPES.get(x.dtype)
-    if dt is None:
-        raise ValueError(f"unsupported dtype {x.dtype}")
-    tokens, k = x.shape
-    dev = x.get_device()
-    xp, ldx = _matrix(x, "x", k, dev)
-    experts = 1 if offsets is None else offsets.numel() - 1
+@functools.lru_cache(maxsize=1024)
+def _product_weight(fmt, experts, n, k, gated):
+    """Format id and packed bytes of a product's weight."""
+    fid = _fmt(fmt)
     if fid not in WEIGHT_FORMATS or n < 1 or k < 1 or experts < 1:
         raise ValueError(f"no product of format {fmt!r} with n={n}, k={k}, {experts} expert(s)")
-    wp = _ptr(w, "w", _weight_bytes(fid, experts * n * (2 if gated else 1), k), dev)
+    return fid, _weight_bytes(fid, experts * n * (2 if gated else 1), k)
+
+
+def _product(fn, fmt, x, w, n, gated, y, offsets, rows, stream):
+    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+        raise ValueError("x must be a device matrix")
+    dtype = x.dtype
+    dt = DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    tokens, k = x.shape
+    dev = x.get_device()
+    n, gated = int(n), bool(gated)
+    experts = 1 if offsets is None else offsets.numel() - 1
+    fid, nbytes = _product_weight(fmt, experts, n, k, gated)
+    xp, ldx = _matrix(x, "x", tokens, k, dev, dtype)
+    wp = _ptr(w, "w", nbytes, dev)
+    slots = tokens if rows is None else rows.numel()
     if y is None:
-        y = _empty((slots, n), x.dtype, x.device, stream)
-    elif y.dim() != 2 or y.shape[0] != slots:
-        raise ValueError(f"y must have {slots} rows")
-    yp, ldy = _matrix(y, "y", n, dev, x.dtype)
+        y = _empty(x, (slots, n), dtype, stream)
+        yp, ldy = y.data_ptr(), n
+    else:
+        yp, ldy = _matrix(y, "y", slots, n, dev, dtype)
     if offsets is None:
-        st = _lib().qr_linear(fid, dt, bool(gated), xp, ldx, wp, yp, ldy, slots, n, k, _stream(stream, dev))
+        st = _lib().qr_linear(fid, dt, gated, xp, ldx, wp, yp, ldy, slots, n, k, _stream(stream, dev))
     else:
         op = _vector(offsets, "offsets", experts + 1, torch.int32, dev)
         rp = None if rows is None else _vector(rows, "rows", slots, torch.int32, dev)
-        st = _lib().qr_experts(fid, dt, bool(gated), xp, ldx, tokens, wp, op, rp, yp, ldy, slots, experts, n, k,
+        st = _lib().qr_experts(fid, dt, gated, xp, ldx, tokens, wp, op, rp, yp, ldy, slots, experts, n, k,
                                _stream(stream, dev))
-    _check(fn, st)
+    if st:
+        _check(fn, st)
     return y
 
 
 def qr_linear(fmt, x, w, n, gated=False, y=None, stream=None):
     """``x`` [m, k] times the packed weight ``w`` [n, k] (``gated``: [2 n, k], the gate
     rows and then the up rows, for silu(gate) * up); returns ``y`` [m, n]."""
-    return _product("qr_linear", fmt, x, w, n, gated, y, len(x), None, None, stream)
+    return _product("qr_linear", fmt, x, w, n, gated, y, None, None, stream)
 
 
 def qr_experts(fmt, x, w, n, offsets, rows=None, gated=False, y=None, stream=None):
@@ -160,8 +171,7 @@ def qr_experts(fmt, x, w, n, offsets, rows=None, gated=False, y=None, stream=Non
     ``w`` is the packed [experts, n, k] weight (``gated``: [experts, 2 n, k]).  Row s of
     the result, for offsets[e] <= s < offsets[e + 1], is row ``rows[s]`` of ``x`` (row s
     without ``rows``) times the weight of expert e; the rows from offsets[-1] on are zero."""
-    return _product("qr_experts", fmt, x, w, n, gated, y, len(x) if rows is None else rows.numel(), offsets, rows,
-                    stream)
+    return _product("qr_experts", fmt, x, w, n, gated, y, offsets, rows, stream)
 
 
 def qr_route(ids, experts, offsets=None, rows=None, pos=None, stream=None):
@@ -181,21 +191,28 @@ def qr_route(ids, experts, offsets=None, rows=None, pos=None, stream=None):
     dev, slots = ids.get_device(), tokens * top
     if experts < 1 or top < 1:
         raise ValueError(f"no plan of {experts} expert(s), {top} a token")
+    i32 = torch.int32
     if offsets is None:
-        offsets = _empty(experts + 1, torch.int32, ids.device, stream)
+        offsets = _empty(ids, (experts + 1,), i32, stream)
     if rows is None:
-        rows = _empty(slots, torch.int32, ids.device, stream)
+        rows = _empty(ids, (slots,), i32, stream)
     if pos is None:
-        pos = _empty((tokens, top), torch.int32, ids.device, stream)
-    op = _vector(offsets, "offsets", experts + 1, torch.int32, dev)
-    rp = _vector(rows, "rows", slots, torch.int32, dev)
-    pp = _vector(pos, "pos", slots, torch.int32, dev)
+        pos = _empty(ids, (tokens, top), i32, stream)
+    op = _vector(offsets, "offsets", experts + 1, i32, dev)
+    rp = _vector(rows, "rows", slots, i32, dev)
+    pp = _vector(pos, "pos", slots, i32, dev)
     L = _lib()
-    nbytes = L.qr_route_workspace(tokens, top, experts)
-    ws = _empty(nbytes, torch.uint8, ids.device, stream) if nbytes else None  # scratch of this call
-    _check("qr_route", L.qr_route(ip, idb, op, rp, pp, tokens, top, experts, ws.data_ptr() if nbytes else None,
-                                  _stream(stream, dev)))
+    nbytes = _route_workspace(tokens, top, experts)
+    ws = _empty(ids, (nbytes,), torch.uint8, stream) if nbytes else None  # scratch of this call
+    st = L.qr_route(ip, idb, op, rp, pp, tokens, top, experts, ws.data_ptr() if nbytes else None, _stream(stream, dev))
+    if st:
+        _check("qr_route", st)
     return offsets, rows, pos
+
+
+@functools.lru_cache(maxsize=1024)
+def _route_workspace(tokens, top, experts):
+    return int(_lib().qr_route_workspace(tokens, top, experts))
 
 
 def qr_combine(y, pos, gates, out=None, stream=None):
@@ -203,19 +220,22 @@ def qr_combine(y, pos, gates, out=None, stream=None):
     ``pos`` int32 and ``gates`` fp32 are [tokens, top], ``y`` [slots, n]."""
     if not (isinstance(y, torch.Tensor) and y.dim() == 2 and isinstance(pos, torch.Tensor) and pos.dim() == 2):
         raise ValueError("y and pos must be device matrices")
-    dt = DTYPES.get(y.dtype)
+    dtype = y.dtype
+    dt = DTYPES.get(dtype)
     if dt is None:
-        raise ValueError(f"unsupported dtype {y.dtype}")
+        raise ValueError(f"unsupported dtype {dtype}")
     slots, n = y.shape
     tokens, top = pos.shape
     dev = y.get_device()
-    yp, ldy = _matrix(y, "y", n, dev)
+    yp, ldy = _matrix(y, "y", slots, n, dev, dtype)
     if out is None:
-        out = _empty((tokens, n), y.dtype, y.device, stream)
-    elif out.dim() != 2 or out.shape[0] != tokens:
-        raise ValueError(f"out must have {tokens} rows")
-    op, ldo = _matrix(out, "out", n, dev, y.dtype)
+        out = _empty(y, (tokens, n), dtype, stream)
+        op, ldo = out.data_ptr(), n
+    else:
+        op, ldo = _matrix(out, "out", tokens, n, dev, dtype)
     pp = _vector(pos, "pos", tokens * top, torch.int32, dev)
     gp = _vector(gates, "gates", tokens * top, torch.float32, dev)
-    _check("qr_combine", _lib().qr_combine(dt, yp, ldy, slots, pp, gp, op, ldo, tokens, top, n, _stream(stream, dev)))
+    st = _lib().qr_combine(dt, yp, ldy, slots, pp, gp, op, ldo, tokens, top, n, _stream(stream, dev))
+    if st:
+        _check("qr_combine", st)
     return out

@@ -40,13 +40,10 @@ static qr_status launch_few(const ProductArgs& a, hipStream_t st) {
   return launch_tiles(few_rows_kernel<F, DT, GATED, 1, NW, KW>, a, 16, 16 * NW / (GATED ? 2 : 1), kWave * NW * KW, st);
 }
 
-template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR>
+template <int F, int DT, bool GATED, int MFR, int NFR, int DEPTH, bool ALIGNED>
 static qr_status launch_many(const ProductArgs& a, hipStream_t st) {
-  // rows of x that begin on 16 bytes go to LDS directly
-  const bool aligned = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0;
-  return launch_tiles(aligned ? many_rows_kernel<F, DT, GATED, WM, WN, MFR, NFR, true>
-                              : many_rows_kernel<F, DT, GATED, WM, WN, MFR, NFR, false>,
-                      a, 16 * WM * MFR, 16 * WN * NFR / (GATED ? 2 : 1), kWave * WM * WN, st);
+  return launch_tiles(many_rows_kernel<F, DT, GATED, 1, 4, MFR, NFR, DEPTH, ALIGNED>, a, 16 * MFR,
+                      64 * NFR / (GATED ? 2 : 1), kWave * 4, st);
 }
 
 template <int F, int DT, bool GATED>
@@ -62,8 +59,13 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
     if (quads >= 192) return launch_few<F, DT, GATED, 4, 4>(a, st);
     return launch_few<F, DT, GATED, GATED ? 2 : 1, GATED ? 4 : 8>(a, st);
   }
-  if (rows <= 96) return launch_many<F, DT, GATED, 2, 2, 2, 4>(a, st);
-  return launch_many<F, DT, GATED, 2, 2, 4, 4>(a, st);
+  // rows of x that begin on 16 bytes and hold whole 16-byte pieces go to LDS
+  // directly, by 32-bit offsets
+  const bool aligned = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0 && a.k % 8 == 0 && a.xrows * a.ldx < (1LL << 31);
+  if (!aligned) return launch_many<F, DT, GATED, 4, 2, 1, false>(a, st);
+  const long long large = row_tiles(a.slots, a.experts, !a.offsets, 128) * ((a.n * (GATED ? 2LL : 1LL) + 255) / 256);
+  if (large >= 192 && (!a.offsets || rows >= 192)) return launch_many<F, DT, GATED, 8, 4, 1, true>(a, st);
+  return launch_many<F, DT, GATED, 4, 2, 2, true>(a, st);
 }
 
 template <int F>

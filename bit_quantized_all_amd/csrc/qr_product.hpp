@@ -26,10 +26,11 @@ namespace qr {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
-// 16-byte accesses at the alignment of a 2-byte value: rows of odd
+// 16- and 8-byte accesses at the alignment of a 2-byte value: rows of odd
 // stride are read and written without a special case (gfx950 serves unaligned
 // global accesses in hardware).
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
+typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 
 constexpr int kChunk = 128;        // values of k that one 16-byte load per lane covers
 constexpr int kChunkBlocks = kChunk / kBlockValues;
@@ -789,22 +790,44 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 // next LDS read of any address, also of the buffer that is not being written;
 // it has no result that a register waits for.  M0 holds the LDS address; nothing
 // else here uses it.  Who reads the bytes waits with loads_done() and a barrier.
-__device__ __forceinline__ void load_to_lds(const uint8_t* p, void* lds) {
-  const uint32_t at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+__device__ __forceinline__ uint32_t lds_address(void* lds) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+}
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "memory");
+}
+// One value of SIZE bytes (1 or 2, zero-extended) from each lane's address to lds + 4 lane.
+template <int SIZE>
+__device__ __forceinline__ void load_value_to_lds(const uint8_t* p, uint32_t lds) {
+  if constexpr (SIZE == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(lds), "v"(p) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(lds), "v"(p) : "memory");
+}
+// The same from a base of the whole wave plus each lane's offset.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(__builtin_amdgcn_readfirstlane(at)), "v"(p)
+               : "s"(lds), "v"(offset), "s"(base)
                : "memory");
 }
-__device__ __forceinline__ void loads_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+// A barrier of the workgroup that leaves loads to LDS on their way, which
+// __syncthreads() would wait for; each wave's LDS accesses are done before it.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+// Waits until at most N of the wave's loads are still on their way (they arrive in order).
+template <int N>
+__device__ __forceinline__ void loads_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
 
 // A workgroup of WM x WN waves computes a tile of WM MFR 16 rows of x by WN NFR
 // 16 weight rows, each wave MFR x NFR fragments of it, in stages of 64 values
-// of k.  A stage's x and codes go to LDS without a stop in registers, the next
-// stage's while this one is multiplied; scales go through a register.  Each
-// wave decodes the weights it multiplies, rounded to the dtype as qr_decode
-// does, straight into the matrix unit's A: they pass LDS once, in 4 bits, and
-// the work of a decode is shared by MFR products.
+// of k.  A stage's x, codes and scales go to LDS without a stop in registers,
+// DEPTH stages ahead.  Each wave decodes the weights it multiplies, rounded to
+// the dtype as qr_decode does, straight into the matrix unit's A: they pass LDS
+// once, in 4 bits, and the work of a decode is shared by MFR products.
 //
 // LDS: row m of x is 8 units of 16 bytes, unit u at place u ^ (m & 7), so that
 // 8 lanes that read one unit of 8 rows hit 8 groups of banks; the lanes that
@@ -834,24 +857,35 @@ __device__ __forceinline__ TileIndex tile_index(int id, int total, int ncols) {
   return {band * kBand + in % height, in / height};
 }
 
-template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR, bool ALIGNED>
+template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR, int DEPTH, bool ALIGNED>
 __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs a) {
-  static_assert(NFR % (GATED ? 4 : 2) == 0, "fragments come in pairs");
   constexpr int WAVES = WM * WN, HALVES = GATED ? 2 : 1;
+  constexpr int OUT = NFR / HALVES;               // column fragments of y of one wave
+  constexpr int PAIR = OUT > 1 ? 2 : 1;
+  static_assert(OUT * HALVES == NFR && OUT % PAIR == 0, "whole pairs of fragments, or one");
   constexpr int BM = 16 * WM * MFR, BN = 16 * WN * NFR;
   constexpr int COLS = 16 * NFR / HALVES;         // columns of y of one wave
   constexpr int XI = BM / 8 / WAVES;              // loads of x of one wave in a stage: 8 rows each
   constexpr int WI = BN / 32;                     // loads of codes of the workgroup: 32 rows each
   static_assert(XI * 8 * WAVES == BM, "the waves share the loads of x evenly");
-  static_assert(WI <= WAVES, "at most one load of codes for each wave");
+  constexpr int WL = (WI + WAVES - 1) / WAVES;    // ... of one wave
+  static_assert(XI <= MFR, "a load of x goes with each row of the first step's products");
+  static_assert(MFR % NFR == 0, "one fragment is decoded every MFR / NFR rows of products");
   constexpr uint32_t TB = Format<F>::kTileBytes;
   constexpr bool kAsym = Format<F>::kAsym;
-  struct Buffer {
-    u32x4 x[BM][8];
+  // codes and scales come a stage earlier than x: the first step of a stage is
+  // decoded while the last of the one before it is multiplied
+  struct Weights {
     u32x4 codes[BN][kStageBlocks];
-    uint32_t scales[BN];  // of both blocks, or the group's scale and zero point
+    uint32_t scales[BN][kStageBlocks];              // of both blocks; the group's, twice
+    uint32_t zeros[kAsym ? BN : 1][kStageBlocks];
   };
-  __shared__ Buffer lds[2];
+  // loads of one stage of one wave
+  constexpr int kLoads = XI + WL * (kAsym ? 3 : 2);
+  static_assert(WI % WAVES == 0, "every wave has as many loads");
+  constexpr int XBUF = DEPTH + 1, WBUF = DEPTH + 2;
+  __shared__ u32x4 lds_x[XBUF][BM][8];
+  __shared__ Weights lds_w[WBUF];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -873,102 +907,162 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     // x: load i of this wave brings rows 8 (XI wave + i) + lane / 8 of the tile,
     // unit (lane & 7) ^ (row & 7); rows past the end repeat the last, rows of no
     // source the first of x
-    const uint8_t* xrow[XI];
     const int unit = (lane & 7) ^ (lane >> 3);
+    const uint8_t* xrow[ALIGNED ? 1 : XI];
+    uint32_t xoff[XI];
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
       const int m = rt.m0 + 8 * (XI * wave + i) + (lane >> 3);
       const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
-      xrow[i] = a.x + 2 * (s < 0 ? 0 : s) * a.ldx + 16 * unit;
+      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * unit;
+      if constexpr (ALIGNED)
+        xoff[i] = (uint32_t)at;
+      else
+        xrow[i] = a.x + at;
     }
-    // weights: row R of the tile is column col(R) of its half; columns past the last repeat it
+    // weights: row R of the tile is a column of its half; columns past the last repeat it
     const long long row0 = (long long)rt.expert * HALVES * a.n;
-    const long long first = (row0 + n0) * a.blocks;
-    const uint8_t* wb = a.w + (first >> 6) * TB;
-    const int R = 32 * wave + (lane >> 1);  // this lane's row, if wave < WI
-    long long wrow = 0;
-    {
+    // load l of this wave brings rows 32 (WAVES l + wave) + lane / 2, block lane & 1
+    const uint8_t* wlane[WL];
+    uint32_t wfirst[WL];
+#pragma unroll
+    for (int l = 0; l < WL; ++l) {
+      const int R = 32 * (WAVES * l + wave) + (lane >> 1);
       const int f = R / 16 % NFR, q = R & 15;
-      const int half = GATED ? f / (NFR / 2) : 0, ff = GATED ? f % (NFR / 2) : f;
-      const int c = n0 + COLS * (R / (16 * NFR)) + 32 * (ff >> 1) + 8 * (q >> 2) + 4 * (ff & 1) + (q & 3);
-      wrow = (long long)half * a.n + (c < a.n ? c : a.n - 1) - n0;
+      const int half = f / OUT, ff = f % OUT;
+      const int in = PAIR == 2 ? 32 * (ff >> 1) + 8 * (q >> 2) + 4 * (ff & 1) + (q & 3) : q;
+      const int c = n0 + COLS * (R / (16 * NFR)) + in;
+      const long long block = (row0 + (long long)half * a.n + (c < a.n ? c : a.n - 1)) * a.blocks;
+      wlane[l] = a.w + (block >> 6) * TB;
+      wfirst[l] = (uint32_t)(block & 63);
     }
-    // its first block, from wb: up rows are n rows further, past 32 bits of bytes
-    const long long wblock = (first & 63) + wrow * a.blocks;
-    const uint8_t* wlane = wb + (wblock >> 6) * TB;
-    const uint32_t wfirst = (uint32_t)(wblock & 63);
 
     const int last = a.blocks - 1;
-    const int stages = (a.blocks + kStageBlocks - 1) / kStageBlocks;
-    uint32_t sv[2] = {0u, 0u};
-    u32x4 xv[XI];
-    // stages whose x cannot go to LDS directly: rows that are not 16-byte
-    // aligned, and the last values of a row
-    auto through_registers = [&](int st) { return !ALIGNED || kStage * (st + 1) > a.k; };
-    auto fetch = [&](int st, Buffer& to) {
-      if (wave < WI) {
-        const int kb = st * kStageBlocks + (lane & 1);
-        const uint32_t b = wfirst + (uint32_t)(kb < last ? kb : last);  // past the last: that one, times zeros of x
-        const uint32_t at = (b >> 6) * TB, in = b & 63;
-        load_to_lds(wlane + (at + in * 16), &to.codes[32 * wave][0]);
-        if constexpr (kAsym) {
-          // both lanes of a row load the same
-          sv[0] = *reinterpret_cast<const uint16_t*>(wlane + (at + Format<F>::kScaleOffset + (in >> 2) * 2));
-          sv[1] = wlane[at + Format<F>::kZeroOffset + (in >> 2)];
-        } else {
-          sv[0] = *reinterpret_cast<const uint16_t*>(wlane + (at + Format<F>::kScaleOffset + in * 2));
-        }
-      }
-      if (through_registers(st)) {
+    const int stages = (a.k + kStage - 1) / kStage;  // each has values of x
+    u32x4 xv[ALIGNED ? 1 : XI];
+    auto fetch_weights = [&](int st, int buf) {
+      const int kb = st * kStageBlocks + (lane & 1);
+      const uint32_t kc = (uint32_t)(kb < last ? kb : last);  // past the last: that one, times zeros of x
+      const uint32_t to = (uint32_t)(sizeof(Weights) * buf);
 #pragma unroll
-        for (int i = 0; i < XI; ++i) xv[i] = load_x8_tail(xrow[i] - 16 * unit, kStage * st + 8 * unit, a.k);
-      } else {
-#pragma unroll
-        for (int i = 0; i < XI; ++i)
-          load_to_lds(xrow[i] + 2 * kStage * (size_t)st, &to.x[8 * (XI * wave + i)][0]);
+      for (int l = 0; l < WL; ++l) {
+        const int part = WAVES * l + wave;
+        const uint32_t b = wfirst[l] + kc, at = (b >> 6) * TB, in = b & 63;
+        load_to_lds(wlane[l] + (at + in * 16), lds_address(&lds_w[0].codes[0][0]) + to + (uint32_t)(1024 * part));
+        load_value_to_lds<2>(wlane[l] + (at + Format<F>::kScaleOffset + (kAsym ? in >> 2 : in) * 2),
+                             lds_address(&lds_w[0].scales[0][0]) + to + (uint32_t)(256 * part));
+        if constexpr (kAsym)
+          load_value_to_lds<1>(wlane[l] + (at + Format<F>::kZeroOffset + (in >> 2)),
+                               lds_address(&lds_w[0].zeros[0][0]) + to + (uint32_t)(256 * part));
       }
     };
-    fetch(0, lds[0]);
-    for (int st = 0; st < stages; ++st) {
-      Buffer& now = lds[st & 1];
-      loads_done();
-      if (wave < WI) {
-        if constexpr (kAsym) {
-          now.scales[R] = sv[0] | sv[1] << 16;
+    // Rows that begin on 16 bytes (ALIGNED) go to LDS directly, and where a row
+    // ends, zeros instead; others pass through registers.
+    auto fetch_x = [&](int st, int buf, int i) {
+      if constexpr (ALIGNED) {
+        const uint32_t to = lds_address(&lds_x[0][0][0]) + (uint32_t)(BM * 128 * buf + 1024 * (XI * wave + i));
+        const uint8_t* from = a.x + 2 * kStage * (size_t)st;
+        if (kStage * (st + 1) <= a.k) {
+          load_to_lds(from, xoff[i], to);
+        } else if (kStage * st + 8 * unit < a.k) {
+          load_to_lds(from, xoff[i], to);
         } else {
-          reinterpret_cast<uint16_t*>(&now.scales[R])[lane & 1] = (uint16_t)sv[0];
+          lds_x[buf][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = u32x4{0u, 0u, 0u, 0u};
         }
+      } else {
+        if (kStage * (st + 1) <= a.k)
+          xv[i] = *reinterpret_cast<const u32x4_any*>(xrow[i] + 2 * kStage * (size_t)st);
+        else
+          xv[i] = load_x8_tail(xrow[i] - 16 * unit, kStage * st + 8 * unit, a.k);
       }
-      if (through_registers(st)) {
+    };
+    u32x4 wv[NFR];
+    uint32_t code[NFR], scale[NFR], zero[NFR];
+    auto read_step = [&](const Weights& w, int b) {
 #pragma unroll
-        for (int i = 0; i < XI; ++i) now.x[8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
+      for (int f = 0; f < NFR; ++f) {
+        const int R = 16 * (NFR * wn + f) + r;
+        code[f] = reinterpret_cast<const uint32_t*>(&w.codes[R][b])[g];
+        scale[f] = w.scales[R][b];
+        zero[f] = kAsym ? w.zeros[kAsym ? R : 0][b] : 0u;
       }
-      __syncthreads();
-      if (st + 1 < stages) fetch(st + 1, lds[(st + 1) & 1]);
+    };
+    auto decode = [&](int f) {
+      RawBlock raw;
+      raw.scale = scale[f];
+      raw.zero = zero[f];
+      return decode_unit<F, DT>(code[f], BlockScale<F, DT>(raw));
+    };
 
-      uint32_t scale[NFR];
+    // the first DEPTH stages of x, and one more of weights
+    fetch_weights(0, 0);
 #pragma unroll
-      for (int f = 0; f < NFR; ++f) scale[f] = now.scales[16 * (NFR * wn + f) + r];
+    for (int d = 0; d < (ALIGNED ? DEPTH : 1); ++d) {
+      fetch_weights(1 + d, 1 + d);
+#pragma unroll
+      for (int i = 0; i < XI; ++i) fetch_x(d < stages ? d : stages - 1, d, i);
+    }
+    for (int st = 0, xb = 0, wb = 0; st < stages; ++st) {  // xb, wb: where stage st's x and weights are
+      if constexpr (ALIGNED) {
+        loads_done<(DEPTH - 1) * kLoads>();
+      } else {
+        loads_done<0>();
+#pragma unroll
+        for (int i = 0; i < XI; ++i) lds_x[xb][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
+      }
+      stage_barrier();
+      if (st == 0) {
+        read_step(lds_w[0], 0);
+#pragma unroll
+        for (int f = 0; f < NFR; ++f) wv[f] = decode(f);
+      }
+      constexpr int ahead = ALIGNED ? DEPTH : 1;
+      const int xn = xb + ahead >= XBUF ? xb + ahead - XBUF : xb + ahead;
+      const int wn1 = wb + 1 == WBUF ? 0 : wb + 1;
+      const int wna = wb + 1 + ahead >= WBUF ? wb + 1 + ahead - WBUF : wb + 1 + ahead;
+      const u32x4(*xs)[8] = &lds_x[xb][16 * MFR * wm + r];
 #pragma unroll
       for (int b = 0; b < kStageBlocks; ++b) {
-        u32x4 wv[NFR];
+        // This step's products, with the next step's decode and the next
+        // stage's loads in between: the matrix unit and the vector unit work
+        // side by side.  The compiler would decode first and multiply then; it
+        // is held to this order.
+        read_step(lds_w[b + 1 < kStageBlocks ? wb : wn1], (b + 1) % kStageBlocks);
+        u32x4 next[NFR], x[MFR];
 #pragma unroll
-        for (int f = 0; f < NFR; ++f) {
-          RawBlock raw;
-          raw.scale = kAsym ? scale[f] & 0xffffu : (scale[f] >> (16 * b)) & 0xffffu;
-          raw.zero = kAsym ? scale[f] >> 16 : 0u;
-          const BlockScale<F, DT> s(raw);
-          const uint32_t code = reinterpret_cast<const uint32_t*>(&now.codes[16 * (NFR * wn + f) + r][b])[g];
-          wv[f] = decode_unit<F, DT>(code, s);
-        }
+        for (int i = 0; i < 2; ++i) x[i] = xs[16 * i][(4 * b + g) ^ (r & 7)];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < MFR; ++i) {
-          const u32x4 x = now.x[16 * (MFR * wm + i) + r][(4 * b + g) ^ (r & 7)];
+          constexpr int kEvery = MFR / NFR;
+          if (i + 2 < MFR) x[i + 2] = xs[16 * (i + 2)][(4 * b + g) ^ (r & 7)];
 #pragma unroll
-          for (int f = 0; f < NFR; ++f) acc[i][f] = mfma<DT>(wv[f], x, acc[i][f]);
+          for (int f = 0; f < NFR; ++f) acc[i][f] = mfma<DT>(wv[f], x[i], acc[i][f]);
+          if (i % kEvery == kEvery - 1) {
+            next[i / kEvery] = decode(i / kEvery);
+            asm volatile("" : "+v"(next[i / kEvery]));
+#pragma unroll
+            for (int j = 0; j < kEvery; ++j) {
+              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+#pragma unroll
+              for (int f = 0; f < NFR; ++f) {
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x002, (24 + kEvery * NFR - 1) / (kEvery * NFR), 0);
+              }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+          }
+          // past the last stage: loads that nobody reads, so that each stage has as many
+          if (b == 0 && i == 0) fetch_weights(st + 1 + ahead, wna);
+          if (b == 0 && i < XI) fetch_x(st + ahead < stages ? st + ahead : stages - 1, xn, i);
         }
+#pragma unroll
+        for (int f = 0; f < NFR; ++f) wv[f] = next[f];
       }
+      xb = xb + 1 == XBUF ? 0 : xb + 1;
+      wb = wn1;
     }
+    loads_done<0>();  // before the workgroup's LDS goes to another
   }
 
 #pragma unroll
@@ -978,22 +1072,27 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     const bool real = !rt.zero && source_row(a, m) >= 0;
     uint8_t* row = a.y + 2 * (long long)m * a.ldy;
 #pragma unroll
-    for (int p = 0; p < NFR / HALVES; p += 2) {
-      float v[8];
+    for (int p = 0; p < OUT; p += PAIR) {
+      float v[4 * PAIR];
 #pragma unroll
-      for (int e = 0; e < 2; ++e)
+      for (int e = 0; e < PAIR; ++e)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const float h = acc[i][p + e][j];
-          v[4 * e + j] = !real ? 0.0f : GATED ? gate(h, acc[i][p + e + (GATED ? NFR / 2 : 0)][j]) : h;
+          v[4 * e + j] = !real ? 0.0f : GATED ? gate(h, acc[i][p + e + (GATED ? OUT : 0)][j]) : h;
         }
-      const int c = n0 + COLS * wn + 16 * p + 8 * g;
-      const u32x4 o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
-      if (c + 8 <= a.n) {
-        *reinterpret_cast<u32x4_any*>(row + 2 * (size_t)c) = o;
+      const int c = n0 + COLS * wn + 16 * p + 4 * PAIR * g;
+      uint32_t o[2 * PAIR];
+#pragma unroll
+      for (int j = 0; j < 2 * PAIR; ++j) o[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
+      if (c + 4 * PAIR <= a.n) {
+        if constexpr (PAIR == 2)
+          *reinterpret_cast<u32x4_any*>(row + 2 * (size_t)c) = u32x4{o[0], o[1], o[2], o[3]};
+        else
+          *reinterpret_cast<u32x2_any*>(row + 2 * (size_t)c) = u32x2{o[0], o[1]};
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
+        for (int j = 0; j < 4 * PAIR; ++j)
           if (c + j < a.n)
             *reinterpret_cast<uint16_t*>(row + 2 * (size_t)(c + j)) = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
       }

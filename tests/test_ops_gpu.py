@@ -129,6 +129,17 @@ def test_linear(qa, fmt, dtype, gated):
 
 @pytest.mark.parametrize("fmt", sorted(GROUP))
 @pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("m,n,k,gated", [(1300, 4500, 200, False), (1290, 2305, 136, True), (2050, 3001, 72, False)])
+def test_linear_many_rows_and_columns(qa, fmt, dtype, m, n, k, gated):
+    wide = n * (2 if gated else 1)
+    p = random_packed(fmt, wide, k, seed=m)
+    x = activations(m, k, dtype, seed=n)
+    y = qa.qr_linear(fmt, x, torch.from_numpy(p.reshape(-1)).cuda(), n, gated=gated)
+    check_product(y, x, weight64(fmt, p, wide, k, dtype), n, gated, dtype, (fmt, dtype, gated, m, n, k))
+
+
+@pytest.mark.parametrize("fmt", sorted(GROUP))
+@pytest.mark.parametrize("dtype", sorted(DT))
 def test_weights_are_the_codec_s(qa, fmt, dtype):
     """A packed weight is qr_encode's, and a unit vector reads out what qr_decode returns."""
     k, rows = 256, 64
@@ -251,6 +262,8 @@ def test_experts(qa, fmt, dtype, gated):
 def test_experts_many_rows(qa, fmt):
     check_experts(qa, fmt, "bf16", True, [700, 0, 1, 513, 256], 272, 544, 300, True, seed=3)
     check_experts(qa, fmt, "fp16", False, [700, 0, 1, 513, 256], 1001, 333, 300, True, seed=4)
+    check_experts(qa, fmt, "bf16", True, [700, 0, 1, 513, 256], 2500, 88, 300, True, seed=5)
+    check_experts(qa, fmt, "fp16", False, [700, 0, 1, 513, 256], 5003, 104, 300, False, seed=6)
 
 
 def test_experts_all_rows_dropped(qa):

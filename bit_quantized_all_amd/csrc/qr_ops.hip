@@ -27,8 +27,8 @@ static qr_status launch_1d(void (*kernel)(P...), long long groups, int threads, 
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
-constexpr int kRouteChunk = 4096;      // slots of one workgroup of a large plan
-constexpr int kRouteSmall = 8192;      // slots up to which one workgroup does it all
+constexpr int kRouteChunk = 2048;      // slots of one workgroup of a large plan
+constexpr int kRouteSmall = 4096;      // slots up to which one workgroup does it all
 static_assert(QR_MAX_EXPERTS <= kRouteThreads, "one thread per expert");
 
 struct RouteArgs {
@@ -80,23 +80,37 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
   __shared__ uint16_t in_wave[kRouteWaves][QR_MAX_EXPERTS];  // of this round
   __shared__ int wave_sum[kRouteWaves];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), wave = tid / kWave;
-  int before = 0;
   if (tid < a.experts) {
-    count[tid] = 0;
+    count[tid] = next[tid] = 0;
     for (int w = 0; w < kRouteWaves; ++w) in_wave[w][tid] = 0;
   }
   __syncthreads();
   if (a.chunks == 1) {
     count_slots<ID>(a, 0, a.slots, count);
     __syncthreads();
-  } else if (tid < a.experts) {
-    int all = 0;
-    for (int c = 0; c < a.chunks; ++c) {
-      const int v = a.counts[(size_t)c * a.experts + tid];
-      if (c < (int)blockIdx.x) before += v;
-      all += v;
+  } else {
+    // An expert's counts are added up by as many threads as there are, 16
+    // loads of each in flight: the loads' latency is what this costs (262144
+    // slots of 256 experts: 23 us with one thread and one load at a time).
+    int width = 1;
+    while (width < a.experts) width <<= 1;
+    const int e = tid & (width - 1), parts = kRouteThreads / width;
+    int before = 0, all = 0;
+    if (e < a.experts) {
+      for (int c0 = tid / width * 16; c0 < a.chunks; c0 += parts * 16) {
+        int v[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[i] = c0 + i < a.chunks ? a.counts[(size_t)(c0 + i) * a.experts + e] : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          all += v[i];
+          before += c0 + i < (int)blockIdx.x ? v[i] : 0;
+        }
+      }
+      atomicAdd(&count[e], all);
+      atomicAdd(&next[e], before);
     }
-    count[tid] = all;
+    __syncthreads();
   }
   // exclusive scan over the experts
   const int mine = tid < a.experts ? count[tid] : 0;
@@ -114,7 +128,7 @@ __global__ __launch_bounds__(kRouteThreads) void route_place_kernel(RouteArgs a)
     if (w < wave) begin += wave_sum[w];
     kept += wave_sum[w];
   }
-  if (tid < a.experts) next[tid] = begin + before;
+  if (tid < a.experts) next[tid] += begin;
   if (blockIdx.x == 0) {
     if (tid < a.experts) a.offsets[tid] = begin;
     if (tid == 0) a.offsets[a.experts] = kept;

@@ -194,13 +194,19 @@ def qr_route(ids, experts, offsets=None, rows=None, pos=None, stream=None):
     i32 = torch.int32
     if offsets is None:
         offsets = _empty(ids, (experts + 1,), i32, stream)
+        op = offsets.data_ptr()
+    else:
+        op = _vector(offsets, "offsets", experts + 1, i32, dev)
     if rows is None:
         rows = _empty(ids, (slots,), i32, stream)
+        rp = rows.data_ptr()
+    else:
+        rp = _vector(rows, "rows", slots, i32, dev)
     if pos is None:
         pos = _empty(ids, (tokens, top), i32, stream)
-    op = _vector(offsets, "offsets", experts + 1, i32, dev)
-    rp = _vector(rows, "rows", slots, i32, dev)
-    pp = _vector(pos, "pos", slots, i32, dev)
+        pp = pos.data_ptr()
+    else:
+        pp = _vector(pos, "pos", slots, i32, dev)
     L = _lib()
     nbytes = _route_workspace(tokens, top, experts)
     ws = _empty(ids, (nbytes,), torch.uint8, stream) if nbytes else None  # scratch of this call

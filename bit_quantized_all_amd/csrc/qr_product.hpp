@@ -459,6 +459,47 @@ __global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
 }
 
 // ---------------------------------------------------------------------------
+// loads that go to LDS
+// ---------------------------------------------------------------------------
+
+// 16 bytes from each lane's address to lds + 16 lane, which is the same for the
+// whole wave.  In assembly, because the compiler would wait for it before the
+// next LDS read of any address, also of the buffer that is not being written;
+// it has no result that a register waits for.  M0 holds the LDS address; nothing
+// else here uses it.  Who reads the bytes waits with loads_done() and a barrier.
+__device__ __forceinline__ uint32_t lds_address(void* lds) {
+  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+}
+__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "memory");
+}
+// One value of SIZE bytes (1 or 2, zero-extended) from each lane's address to lds + 4 lane.
+template <int SIZE>
+__device__ __forceinline__ void load_value_to_lds(const uint8_t* p, uint32_t lds) {
+  if constexpr (SIZE == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(lds), "v"(p) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(lds), "v"(p) : "memory");
+}
+// The same from a base of the whole wave plus each lane's offset.
+__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+               :
+               : "s"(lds), "v"(offset), "s"(base)
+               : "memory");
+}
+// A barrier of the workgroup that leaves loads to LDS on their way, which
+// __syncthreads() would wait for; each wave's LDS accesses are done before it.
+__device__ __forceinline__ void stage_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+}
+// Waits until at most N of the wave's loads are still on their way (they arrive in order).
+template <int N>
+__device__ __forceinline__ void loads_done() {
+  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
+}
+
+// ---------------------------------------------------------------------------
 // few rows
 // ---------------------------------------------------------------------------
 
@@ -525,105 +566,122 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 // One workgroup multiplies 16 MF rows of x by NW fragments of 16 weight rows
 // (gated: NW / 2 of the gate rows and as many of the up rows).  Its KW x NW
 // waves share the k axis in KW groups (group kw takes every KW-th segment of
-// 512 values); a wave has one weight fragment, and the waves of a group share
+// 256 values); a wave has one weight fragment, and the waves of a group share
 // the segment's x.  The groups' sums are joined through LDS in their order.
-//
-// Here x is the matrix unit's A and the weight its B, so that a lane's results
-// belong to the weight row whose blocks it loads: lane (r, g) has rows
-// 4 g .. 4 g + 3 of x and weight row r.  Of chunk c of a segment it loads block
-// 4 c + g; after exchange_units() product i of the chunk is block 4 c + i.
 //
 // Requests are dear: a load takes the CU's address unit a cycle for every
 // 64-byte piece it touches, 16 when four neighbouring lanes share one and 64
 // when each lane reads a row of its own, as the fragments of the matrix unit
-// want it.  The codes are loaded that way (a 16-byte piece lasts for four
-// products), x and the scales are not: lane 4 r + u loads them (unit u of row
-// r) and hands them to lane (r, g = u), x through LDS and the scales by a lane
-// permutation.
+// want it.  So nothing is loaded in fragment order: codes, scales and x go to
+// LDS in whole runs of a row, DEPTH segments ahead.  There, 16-byte piece p of
+// row r (a block of codes, a unit of x) lies at place p ^ (r & 7), so that lanes
+// which read one piece of eight rows hit eight different groups of banks; the
+// lanes that load it take their pieces in that order.
+//
+// x is the matrix unit's A here and the weight its B, so that a lane's results
+// belong to one weight row, whose scales it applies to them: lane (r, g) has
+// rows 4 g .. 4 g + 3 of x and weight row r.  It reads codes of blocks 2 g + j,
+// j = 0, 1, of a segment; after exchange_units() product i of step j is block
+// 2 i + j.
 //
 // sum_k x (c - z) is taken as sum_k x c - z sum_k x: the codes need no
 // subtraction, and sum_k x comes from one more product.  An infinity in x
 // would make that inf - inf; a wave whose sum is not finite computes it again
 // with the values c - z themselves.
-constexpr int kSegment = 512;
+constexpr int kSegment = 256;
 constexpr int kSegBlocks = kSegment / kBlockValues;
+constexpr int kSegUnits = kSegment / 8;
 
-template <int F, int DT, int MF, int NW, int KW>
+template <int F, int DT, int MF, int NW, int KW, int DEPTH, bool ALIGNED>
 struct FewRows {
   static constexpr bool kAsym = Format<F>::kAsym;
   static constexpr bool kZeros = !Format<F>::kFp4;  // codes have a zero point
-  static constexpr int XL = MF * kSegBlocks / NW;   // loads of x of one wave in a segment
-  static_assert(XL * NW == MF * kSegBlocks, "the waves of a group share the loads of x evenly");
-  // a wave that has x to itself writes it when it is done with the last segment;
-  // waves that share it write one copy while some still read the other
-  static constexpr int XB = NW == 1 ? 1 : 2;
+  static constexpr int XL = MF * 8 / NW;            // loads of x of one wave in a segment: two rows each
+  static_assert(XL * NW == MF * 8, "the waves of a group share the loads of x evenly");
+  static constexpr int kLoads = XL + 4;             // loads of one wave in a segment
+  static constexpr int BUF = DEPTH + 1;
+  struct Wave {
+    u32x4 codes[16][kSegBlocks];
+    uint32_t scales[16][kSegBlocks];  // asymmetric: [row][group] scales and, 64 words on, zero points
+  };
+  struct Buffer {
+    u32x4 x[KW][16 * MF][kSegUnits];
+    Wave w[KW][NW];
+  };
   union Stage {
-    u32x4 x[XB][KW][MF * kSegBlocks][16][4];  // [block][row][unit]
-    f32x4 sums[KW][NW][MF][kWave];            // ... and when x is done with, the waves' sums
+    Buffer buffer[BUF];
+    f32x4 sums[KW][NW][MF][kWave];  // when all is multiplied
   };
 
-  const uint8_t* xrow[MF];  // row lane >> 2 of each fragment
-  bool here[MF];            // ... if there is one
   const uint8_t* w;
-  uint32_t cblock;          // first block of weight row lane & 15, from w
-  uint32_t sblock;          // the same of row lane >> 2, whose scales this lane loads
+  uint32_t cblock[2];  // first block of weight rows lane / 8 and 8 + lane / 8, from w
+  uint32_t gblock;     // the same of row lane / 2 % 16 (asymmetric: scales)
+  const uint8_t* xrow[ALIGNED ? 1 : XL];  // of each load: its row of x, at this lane's unit
+  uint32_t xoff[XL];                      // ... from x
+  u32x4 xv[ALIGNED ? 1 : XL];
   f32x4 acc[MF];
 
-  struct Loads {
-    u32x4 codes[4];
-    uint32_t s[4];  // scales of blocks 4 u .. 4 u + 3, or their group's scale and zero point
-    u32x4 x[XL];
-  };
+  __device__ __forceinline__ static int unit_of(int lane, int t, int nw) {
+    return (lane & 31) ^ ((2 * (nw + NW * t) + (lane >> 5)) & 7);
+  }
 
-  __device__ __forceinline__ void fetch(const ProductArgs& a, Loads& l, int seg, int nw, int lane) const {
+  __device__ __forceinline__ void fetch(const ProductArgs& a, Buffer& to, int seg, int kw, int nw, int lane) {
     constexpr uint32_t TB = Format<F>::kTileBytes;
-    const int last = a.blocks - 1, u = lane & 3, g = lane >> 4;
+    const int last = a.blocks - 1;
     // a block past the row's last: that block again, times zeros of x
+    auto clamp = [&](int kb) { return (uint32_t)(kb < last ? kb : last); };
+    const uint32_t codes = lds_address(&to.w[kw][nw].codes[0][0]), scales = lds_address(&to.w[kw][nw].scales[0][0]);
+    const uint32_t kc = clamp(seg * kSegBlocks + ((lane & 7) ^ (lane >> 3)));
+    const uint32_t ks = clamp(seg * kSegBlocks + (kAsym ? 4 * (lane & 1) : lane & 7));
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-      const int kb = seg * kSegBlocks + kChunkBlocks * c + g;
-      const uint32_t b = cblock + (uint32_t)(kb < last ? kb : last);
-      l.codes[c] = *reinterpret_cast<const u32x4*>(w + ((b >> 6) * TB + (b & 63) * 16));
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t b = cblock[q] + kc;
+      load_to_lds(w + ((b >> 6) * TB + (b & 63) * 16), codes + 1024 * q);
     }
-    const int kb = seg * kSegBlocks + kChunkBlocks * u;
     if constexpr (kAsym) {
-      const uint32_t b = sblock + (uint32_t)(kb < last ? kb : last);
-      const uint32_t tile = (b >> 6) * TB, in = (b & 63) >> 2;
-      l.s[0] = *reinterpret_cast<const uint16_t*>(w + (tile + Format<F>::kScaleOffset + in * 2));
-      l.s[1] = w[tile + Format<F>::kZeroOffset + in];
-    } else if ((a.blocks & 3) == 0) {
-      // rows of whole groups of four: their scales are one aligned load
-      const uint32_t b = sblock + (uint32_t)(kb < last ? kb : last - 3);
-      const u32x2 v = *reinterpret_cast<const u32x2*>(w + ((b >> 6) * TB + Format<F>::kScaleOffset + (b & 63) * 2));
-      l.s[0] = v.x;
-      l.s[2] = v.y;
-      l.s[1] = l.s[3] = 0;
+      const uint32_t b = gblock + ks, tile = (b >> 6) * TB, in = (b & 63) >> 2;
+      load_value_to_lds<2>(w + (tile + Format<F>::kScaleOffset + in * 2), scales);
+      load_value_to_lds<1>(w + (tile + Format<F>::kZeroOffset + in), scales + 256);
     } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t b = sblock + (uint32_t)(kb + j < last ? kb + j : last);
-        l.s[j] = *reinterpret_cast<const uint16_t*>(w + ((b >> 6) * TB + Format<F>::kScaleOffset + (b & 63) * 2));
+      for (int q = 0; q < 2; ++q) {
+        const uint32_t b = cblock[q] + ks;
+        load_value_to_lds<2>(w + ((b >> 6) * TB + Format<F>::kScaleOffset + (b & 63) * 2), scales + 256 * q);
       }
     }
-    // unit u of some of the segment's blocks, of row lane >> 2
-    const int k0 = kSegment * seg + 8 * u;
     const bool whole = kSegment * (seg + 1) <= a.k;
+    if constexpr (ALIGNED) {
+      const uint8_t* from = a.x + 2 * kSegment * (size_t)seg;
+      const uint32_t x = lds_address(&to.x[kw][0][0]);
+      if (whole) {
 #pragma unroll
-    for (int t = 0; t < XL; ++t) {
-      const int q = nw + NW * t, m = q / kSegBlocks, k = k0 + kBlockValues * (q % kSegBlocks);
-      l.x[t] = u32x4{0u, 0u, 0u, 0u};
-      if (m ? here[MF - 1] : here[0]) {
-        const uint8_t* row = m ? xrow[MF - 1] : xrow[0];
-        if (whole)
-          l.x[t] = *reinterpret_cast<const u32x4_any*>(row + 2 * (size_t)k);
-        else
-          l.x[t] = load_x8_tail(row, k, a.k);
+        for (int t = 0; t < XL; ++t) load_to_lds(from, xoff[t], x + 1024 * (nw + NW * t));
+      } else {
+#pragma unroll
+        for (int t = 0; t < XL; ++t) {
+          const int q = nw + NW * t;
+          if (kSegment * seg + 8 * unit_of(lane, t, nw) < a.k)
+            load_to_lds(from, xoff[t], x + 1024 * q);
+          else
+            to.x[kw][2 * q + (lane >> 5)][lane & 31] = u32x4{0u, 0u, 0u, 0u};
+        }
+      }
+    } else {
+      if (whole) {
+#pragma unroll
+        for (int t = 0; t < XL; ++t)
+          xv[t] = *reinterpret_cast<const u32x4_any*>(xrow[t] + 2 * kSegment * (size_t)seg);
+      } else {
+#pragma unroll
+        for (int t = 0; t < XL; ++t) {
+          const int unit = unit_of(lane, t, nw);
+          xv[t] = load_x8_tail(xrow[t] - 16 * unit, kSegment * seg + 8 * unit, a.k);
+        }
       }
     }
   }
 
-  // Adds this wave's share to acc.  All of the next segment loads while one is
-  // multiplied.
+  // Adds this wave's share to acc.
   template <bool SIGNED>
   __device__ __forceinline__ void sum(const ProductArgs& a, Stage& stage, int kw, int nw, int lane) {
     const int r = lane & 15, g = lane >> 4;
@@ -634,74 +692,88 @@ struct FewRows {
     const uint32_t factor = kAsym ? (DT == kFp16 ? 0x3C003C00u : 0x3F803F80u)   // 1
                                   : (DT == kFp16 ? 0xC800C800u : 0xC100C100u);  // -8
     const u32x4 factors = {factor, factor, factor, factor};
-    const int segments = (a.blocks + kSegBlocks - 1) / kSegBlocks;
-    Loads l;
-    if (kw < segments) fetch(a, l, kw, nw, lane);
+    const int segments = (a.k + kSegment - 1) / kSegment;  // each has values of x
+    constexpr int ahead = ALIGNED ? DEPTH : 1;
+#pragma unroll
+    for (int d = 0; d < ahead; ++d)
+      if (d * KW + kw < segments) fetch(a, stage.buffer[d], d * KW + kw, kw, nw, lane);
     // every wave goes through as many rounds as the first group
-    for (int s0 = 0, buf = 0; s0 < segments; s0 += KW, buf ^= 1) {
+    for (int s0 = 0, buf = 0; s0 < segments; s0 += KW, buf = buf + 1 == BUF ? 0 : buf + 1) {
       const int seg = s0 + kw;
-      u32x4 codes[4], sc[2];
-      if (seg < segments) {
-#pragma unroll
-        for (int t = 0; t < XL; ++t) stage.x[buf % XB][kw][nw + NW * t][lane >> 2][(lane & 3) ^ (lane >> 4)] = l.x[t];
-#pragma unroll
-        for (int h = 0; h < (kAsym ? 1 : 2); ++h) {
-          // from lane 4 r + u to lane (r, u), and from row r's four lanes to each of them
-          const uint32_t s =
-              (uint32_t)__builtin_amdgcn_ds_bpermute(4 * (4 * r + g), (int)(l.s[2 * h] | l.s[2 * h + 1] << 16));
-          sc[h] = exchange_units(u32x4{s, s, s, s});
-        }
-#pragma unroll
-        for (int c = 0; c < 4; ++c) codes[c] = exchange_units(l.codes[c]);
-      }
-      if constexpr (NW == 1)
-        wave_lds_sync();
+      Buffer& now = stage.buffer[buf];
+      if (ahead == 2 && seg + KW < segments)
+        loads_done<kLoads>();
       else
-        __syncthreads();
-      if (seg + KW < segments) fetch(a, l, seg + KW, nw, lane);
-      if (seg < segments) {
-        const u32x4(*xs)[16][4] = stage.x[buf % XB][kw];
+        loads_done<0>();
+      if constexpr (!ALIGNED) {
+        if (seg < segments) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          f32x4 part[MF], sx[MF];  // of the asymmetric format's group
-          const float z = kAsym ? (float)(sc[0][c] >> 16) : 8.0f;
+          for (int t = 0; t < XL; ++t) now.x[kw][2 * (nw + NW * t) + (lane >> 5)][lane & 31] = xv[t];
+        }
+      }
+      stage_barrier();
+      const int next = buf + ahead >= BUF ? buf + ahead - BUF : buf + ahead;
+      if (seg + ahead * KW < segments) fetch(a, stage.buffer[next], seg + ahead * KW, kw, nw, lane);
+      if (seg >= segments) continue;
+      const Wave& mine = now.w[kw][nw];
+      u32x4 codes[2];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const u32x4 wv = unit_values<F, DT, SIGNED>(codes[c][i], z);
-            const float d =
-                (float)__builtin_bit_cast(_Float16, (uint16_t)(kAsym ? sc[0][c] : sc[i >> 1][c] >> (16 * (i & 1))));
+      for (int j = 0; j < 2; ++j) codes[j] = exchange_units(mine.codes[r][(2 * g + j) ^ (r & 7)]);
+      uint32_t scale[kAsym ? 2 : 8], zero[2];
+      if constexpr (kAsym) {
+        const uint32_t* sc = &mine.scales[0][0];
 #pragma unroll
-            for (int m = 0; m < MF; ++m) {
-              const u32x4 x = xs[m * kSegBlocks + 4 * c + i][r][g ^ (r >> 2)];
-              if constexpr (kAsym && !SIGNED) {
-                part[m] = mfma<DT>(x, wv, i ? part[m] : none);
-                sx[m] = mfma<DT>(x, factors, i ? sx[m] : none);
-              } else {
-                f32x4 p = none;
-                if constexpr (kZeros && !SIGNED) p = mfma<DT>(x, factors, none);
-                p = mfma<DT>(x, wv, p);
+        for (int h = 0; h < 2; ++h) {
+          scale[h] = sc[2 * r + h];
+          zero[h] = sc[64 + 2 * r + h];
+        }
+      } else {
 #pragma unroll
-                for (int t = 0; t < 4; ++t) acc[m][t] = __builtin_fmaf(d, p[t], acc[m][t]);
-              }
+        for (int h = 0; h < 2; ++h) {
+          const u32x4 v = *reinterpret_cast<const u32x4*>(&mine.scales[r][4 * h]);
+          scale[4 * h] = v.x; scale[4 * h + 1] = v.y; scale[4 * h + 2] = v.z; scale[4 * h + 3] = v.w;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {  // the asymmetric format's groups: blocks 4 h .. 4 h + 3
+        f32x4 part[MF], sx[MF];
+        const float z = kAsym ? (float)zero[h] : 8.0f;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int b = 4 * h + q, i = b >> 1, j = b & 1;
+          const u32x4 wv = unit_values<F, DT, SIGNED>(codes[j][i], z);
+          const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)scale[kAsym ? h : b]);
+#pragma unroll
+          for (int m = 0; m < MF; ++m) {
+            const u32x4 x = now.x[kw][16 * m + r][(4 * b + g) ^ (r & 7)];
+            if constexpr (kAsym && !SIGNED) {
+              part[m] = mfma<DT>(x, wv, q ? part[m] : none);
+              sx[m] = mfma<DT>(x, factors, q ? sx[m] : none);
+            } else {
+              f32x4 p = none;
+              if constexpr (kZeros && !SIGNED) p = mfma<DT>(x, factors, none);
+              p = mfma<DT>(x, wv, p);
+#pragma unroll
+              for (int t = 0; t < 4; ++t) acc[m][t] = __builtin_fmaf(d, p[t], acc[m][t]);
             }
           }
-          if constexpr (kAsym && !SIGNED) {
-            const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)sc[0][c]);
+        }
+        if constexpr (kAsym && !SIGNED) {
+          const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)scale[h]);
 #pragma unroll
-            for (int m = 0; m < MF; ++m)
+          for (int m = 0; m < MF; ++m)
 #pragma unroll
-              for (int t = 0; t < 4; ++t)
-                acc[m][t] = __builtin_fmaf(d, __builtin_fmaf(-z, sx[m][t], part[m][t]), acc[m][t]);
-          }
+            for (int t = 0; t < 4; ++t)
+              acc[m][t] = __builtin_fmaf(d, __builtin_fmaf(-z, sx[m][t], part[m][t]), acc[m][t]);
         }
       }
     }
   }
 };
 
-template <int F, int DT, bool GATED, int MF, int NW, int KW>
+template <int F, int DT, bool GATED, int MF, int NW, int KW, int DEPTH, bool ALIGNED>
 __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) {
-  using T = FewRows<F, DT, MF, NW, KW>;
+  using T = FewRows<F, DT, MF, NW, KW, DEPTH, ALIGNED>;
   constexpr int HALVES = GATED ? 2 : 1;
   constexpr int NF = NW / HALVES;  // column fragments of y
   __shared__ typename T::Stage stage;
@@ -718,11 +790,15 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
   if (!rt.zero) {
     T t;
 #pragma unroll
-    for (int i = 0; i < MF; ++i) {
-      const int m = rt.m0 + 16 * i + (lane >> 2);
-      const long long s = m < rt.m1 ? source_row(a, m) : -1LL;
-      t.here[i] = s >= 0;
-      t.xrow[i] = a.x + 2 * (t.here[i] ? s : 0) * a.ldx;
+    for (int i = 0; i < T::XL; ++i) {
+      // rows past the end repeat the last, rows of no source the first of x
+      const int m = rt.m0 + 2 * (nw + NW * i) + (lane >> 5);
+      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
+      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * T::unit_of(lane, i, nw);
+      if constexpr (ALIGNED)
+        t.xoff[i] = (uint32_t)at;
+      else
+        t.xrow[i] = a.x + at;
     }
     const int c0 = n0 + 16 * (nw % NF);  // first weight row of the wave, of the gate or the up rows
     const long long row0 = ((long long)rt.expert * HALVES + nw / NF) * a.n;
@@ -732,8 +808,9 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
     auto block_of = [&](int c) {
       return (uint32_t)(first & 63) + (uint32_t)((c < a.n ? c : a.n - 1) - n0) * (uint32_t)a.blocks;
     };
-    t.sblock = block_of(c0 + (lane >> 2));
-    t.cblock = block_of(c0 + r);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) t.cblock[q] = block_of(c0 + 8 * q + (lane >> 3));
+    t.gblock = block_of(c0 + (lane >> 1) % 16);
     t.template sum<false>(a, stage, kw, nw, lane);
     if constexpr (T::kZeros) {
       bool finite = true;
@@ -755,7 +832,7 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
             if (__builtin_fabsf(was[i][j]) < __builtin_inff()) t.acc[i][j] = was[i][j];
       }
     }
-    __syncthreads();  // every wave is done with x
+    __syncthreads();  // every wave is done with the segments
 #pragma unroll
     for (int i = 0; i < MF; ++i) stage.sums[kw][nw][i][lane] = t.acc[i];
   }
@@ -776,51 +853,16 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int m = rt.m0 + 16 * i + 4 * g + j;
+    if (m >= rt.m1 || c >= a.n) continue;
     const float v = GATED ? gate(s[0][j], s[HALVES - 1][j]) : s[0][j];
-    if (m < rt.m1 && c < a.n) *reinterpret_cast<uint16_t*>(a.y + 2 * (m * a.ldy + c)) = (uint16_t)pack2<DT>(v, 0.0f);
+    const bool real = !rt.zero && source_row(a, m) >= 0;
+    *reinterpret_cast<uint16_t*>(a.y + 2 * (m * a.ldy + c)) = (uint16_t)pack2<DT>(real ? v : 0.0f, 0.0f);
   }
 }
 
 // ---------------------------------------------------------------------------
 // many rows
 // ---------------------------------------------------------------------------
-
-// 16 bytes from each lane's address to lds + 16 lane, which is the same for the
-// whole wave.  In assembly, because the compiler would wait for it before the
-// next LDS read of any address, also of the buffer that is not being written;
-// it has no result that a register waits for.  M0 holds the LDS address; nothing
-// else here uses it.  Who reads the bytes waits with loads_done() and a barrier.
-__device__ __forceinline__ uint32_t lds_address(void* lds) {
-  return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-}
-__device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "memory");
-}
-// One value of SIZE bytes (1 or 2, zero-extended) from each lane's address to lds + 4 lane.
-template <int SIZE>
-__device__ __forceinline__ void load_value_to_lds(const uint8_t* p, uint32_t lds) {
-  if constexpr (SIZE == 2)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(lds), "v"(p) : "memory");
-  else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(lds), "v"(p) : "memory");
-}
-// The same from a base of the whole wave plus each lane's offset.
-__device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-               :
-               : "s"(lds), "v"(offset), "s"(base)
-               : "memory");
-}
-// A barrier of the workgroup that leaves loads to LDS on their way, which
-// __syncthreads() would wait for; each wave's LDS accesses are done before it.
-__device__ __forceinline__ void stage_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
-}
-// Waits until at most N of the wave's loads are still on their way (they arrive in order).
-template <int N>
-__device__ __forceinline__ void loads_done() {
-  asm volatile("s_waitcnt vmcnt(%0)" : : "n"(N) : "memory");
-}
 
 // A workgroup of WM x WN waves computes a tile of WM MFR 16 rows of x by WN NFR
 // 16 weight rows, each wave MFR x NFR fragments of it, in stages of 64 values

@@ -772,7 +772,7 @@ struct FewRows {
 };
 
 template <int F, int DT, bool GATED, int MF, int NW, int KW, int DEPTH, bool ALIGNED>
-__global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) {
+__global__ __launch_bounds__(kWave* NW* KW, 2) void few_rows_kernel(ProductArgs a) {
   using T = FewRows<F, DT, MF, NW, KW, DEPTH, ALIGNED>;
   constexpr int HALVES = GATED ? 2 : 1;
   constexpr int NF = NW / HALVES;  // column fragments of y

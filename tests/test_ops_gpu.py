@@ -545,3 +545,28 @@ def test_refusals(qa):
     with pytest.raises(qa.QRError) as e:
         qa.qr_combine(x, ids, gates, out=x)
     assert e.value.status == qa.QR_ERR_ALIAS
+
+
+@pytest.mark.parametrize("fmt", sorted(GROUP))
+def test_example_layer(qa, fmt):
+    """The tensor-parallel layer of examples/, against the same layer in fp32.  Quantized
+    weights differ by up to half a step: a block of 32 normal values has a step of its
+    largest value (near 2.3 standard deviations) / 8, a group of 128 (2 x 2.6) / 15, that
+    is 0.29 and 0.35, uniform errors of 0.08 and 0.10 of a value; FP4's steps are 0.5 to 2 of
+    its largest value / 6, near 0.12.  Two layers of them, and the 8-bit wire, stay
+    under twice the larger of these."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "tensor_parallel_moe.py")
+    spec = importlib.util.spec_from_file_location("tensor_parallel_moe", path)
+    ex = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(ex)
+    err = ex.main(["--fmt", fmt, "--tokens", "64", "--ranks", "2", "--width", "512", "--inner", "256", "--experts", "6"])
+    assert err < 0.25
+    x, gate_up, down, ids, gates = ex.make(32, 512, 256, 6, 2, torch.float16, "cuda", seed=1)
+    whole, halves = [ex.Rank(fmt, gate_up, down, 0, 256)], [ex.Rank(fmt, gate_up, down, 0, 128),
+                                                            ex.Rank(fmt, gate_up, down, 128, 256)]
+    one, two = ex.layer(whole, x, ids, gates, 6).float(), ex.layer(halves, x, ids, gates, 6).float()
+    # the same weights in two parts: what differs is the 8-bit wire (a step of 1/128 of a block's
+    # largest value on each rank and on the sum) and fp16 roundings
+    assert ((one - two).norm() / one.norm()).item() < 0.03

@@ -35,11 +35,32 @@ static qr_status launch_rows(const ProductArgs& a, hipStream_t st) {
   return launch_row<F, DT, GATED, MR, 4>(a, st);
 }
 
-template <int F, int DT, bool GATED, int MF, int NW, int KW>
-static qr_status launch_few(bool aligned, const ProductArgs& a, hipStream_t st) {
-  return launch_tiles(aligned ? few_rows_kernel<F, DT, GATED, MF, NW, KW, 1, true>
-                              : few_rows_kernel<F, DT, GATED, MF, NW, KW, 1, false>,
-                      a, 16 * MF, 16 * NW / (GATED ? 2 : 1), kWave * NW * KW, st);
+template <int F, int DT, bool GATED, int MF, int NW, int KW, bool ALIGNED>
+static qr_status launch_few(const ProductArgs& a, hipStream_t st) {
+  return launch_tiles(few_rows_kernel<F, DT, GATED, MF, NW, KW, 1, ALIGNED>, a, 16 * MF, 16 * NW / (GATED ? 2 : 1),
+                      kWave * NW * KW, st);
+}
+
+// Workgroups of four weight fragments and 16 rows: `quads`.
+template <int F, int DT, bool GATED, bool ALIGNED>
+static qr_status launch_few_rows(int rows, const ProductArgs& a, hipStream_t st) {
+  const long long quads = row_tiles(a.slots, a.experts, !a.offsets, 16) * ((a.n + 63) / 64) * (GATED ? 2 : 1);
+  if (rows > 16 && quads > 256) {
+    // two fragments of rows share a weight's decode: 64 experts with 25 rows
+    // each 55 us instead of 74, 100 rows of 4096 x 4096 17 instead of 22; with
+    // 8 rows an expert 52 instead of 46
+    if (quads >= 2048) return launch_few<F, DT, GATED, 2, 8, 1, ALIGNED>(a, st);
+    return launch_few<F, DT, GATED, 2, 4, 2, ALIGNED>(a, st);
+  }
+  // As many waves share the k axis as it takes to have 4096 waves in all:
+  // 16384 rows of 8192, 16 rows of x: 23 us with four, 30 with twice as many
+  // workgroups of half the waves; 4096 x 4096 and 8 rows 7.6 us with one
+  // fragment a workgroup, 8.6 with two, 13 with four
+  if (quads >= 1024) return launch_few<F, DT, GATED, 1, 4, 1, ALIGNED>(a, st);
+  if (quads >= 192) return launch_few<F, DT, GATED, 1, 4, 4, ALIGNED>(a, st);
+  // (one wave would need over 256 registers for rows that pass through them)
+  if constexpr (ALIGNED && !GATED) return launch_few<F, DT, GATED, 1, 1, 4, ALIGNED>(a, st);
+  return launch_few<F, DT, GATED, 1, 2, 4, ALIGNED>(a, st);
 }
 
 template <int F, int DT, bool GATED, int MFR, int NFR, int DEPTH, bool ALIGNED>
@@ -61,24 +82,8 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, 64) * ((a.n * (GATED ? 2LL : 1LL) + 127) / 128);
   // Few rows, or so few tiles of 64 x 128 that they would leave most CUs idle:
   // 64 rows of 8192 x 8192 32 us here, 74 tiled; 300 rows of 4096 x 4096 50 and 41
-  if (rows <= 32 || (rows <= 128 && tiles < 128)) {
-    // workgroups of four weight fragments and 16 rows
-    const long long quads = row_tiles(a.slots, a.experts, !a.offsets, 16) * ((a.n + 63) / 64) * (GATED ? 2 : 1);
-    if (rows > 16 && quads > 256) {
-      // two fragments of rows share a weight's decode: 64 experts with 25 rows
-      // each 55 us instead of 74, 100 rows of 4096 x 4096 17 instead of 22; with
-      // 8 rows an expert 52 instead of 46
-      if (quads >= 2048) return launch_few<F, DT, GATED, 2, 8, 1>(aligned, a, st);
-      return launch_few<F, DT, GATED, 2, 4, 2>(aligned, a, st);
-    }
-    // As many waves share the k axis as it takes to have 4096 waves in all:
-    // 16384 rows of 8192, 16 rows of x: 23 us with four, 30 with twice as many
-    // workgroups of half the waves; 4096 x 4096 and 8 rows 7.6 us with one
-    // fragment a workgroup, 13 with four
-    if (quads >= 1024) return launch_few<F, DT, GATED, 1, 4, 1>(aligned, a, st);
-    if (quads >= 192) return launch_few<F, DT, GATED, 1, 4, 4>(aligned, a, st);
-    return launch_few<F, DT, GATED, 1, GATED ? 2 : 1, 4>(aligned, a, st);
-  }
+  if (rows <= 32 || (rows <= 128 && tiles < 128))
+    return aligned ? launch_few_rows<F, DT, GATED, true>(rows, a, st) : launch_few_rows<F, DT, GATED, false>(rows, a, st);
   if (!aligned) return launch_many<F, DT, GATED, 4, 2, 1, false>(a, st);
   const long long large = row_tiles(a.slots, a.experts, !a.offsets, 128) * ((a.n * (GATED ? 2LL : 1LL) + 255) / 256);
   if (large >= 192 && (!a.offsets || rows >= 192)) return launch_many<F, DT, GATED, 8, 4, 1, true>(a, st);

@@ -772,7 +772,7 @@ struct FewRows {
 };
 
 template <int F, int DT, bool GATED, int MF, int NW, int KW, int DEPTH, bool ALIGNED>
-__global__ __launch_bounds__(kWave* NW* KW, 2) void few_rows_kernel(ProductArgs a) {
+__global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) {
   using T = FewRows<F, DT, MF, NW, KW, DEPTH, ALIGNED>;
   constexpr int HALVES = GATED ? 2 : 1;
   constexpr int NF = NW / HALVES;  // column fragments of y
@@ -837,26 +837,27 @@ __global__ __launch_bounds__(kWave* NW* KW, 2) void few_rows_kernel(ProductArgs 
     for (int i = 0; i < MF; ++i) stage.sums[kw][nw][i][lane] = t.acc[i];
   }
   __syncthreads();
-  // fragment (i, f) of y is joined and stored by wave i NF + f
-  if (wave >= MF * NF) return;
-  const int i = wave / NF, f = wave % NF;
-  f32x4 s[HALVES];
+  // fragment (i, f) of y is joined and stored by wave (i NF + f) % (KW NW)
+  for (int frag = wave; frag < MF * NF; frag += KW * NW) {
+    const int i = frag / NF, f = frag % NF;
+    f32x4 s[HALVES];
 #pragma unroll
-  for (int h = 0; h < HALVES; ++h) {
-    s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    if (!rt.zero) {
+    for (int h = 0; h < HALVES; ++h) {
+      s[h] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (!rt.zero) {
 #pragma unroll
-      for (int k = 0; k < KW; ++k) s[h] += stage.sums[k][h * NF + f][i][lane];
+        for (int k = 0; k < KW; ++k) s[h] += stage.sums[k][h * NF + f][i][lane];
+      }
     }
-  }
-  const int c = n0 + 16 * f + r;
+    const int c = n0 + 16 * f + r;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int m = rt.m0 + 16 * i + 4 * g + j;
-    if (m >= rt.m1 || c >= a.n) continue;
-    const float v = GATED ? gate(s[0][j], s[HALVES - 1][j]) : s[0][j];
-    const bool real = !rt.zero && source_row(a, m) >= 0;
-    *reinterpret_cast<uint16_t*>(a.y + 2 * (m * a.ldy + c)) = (uint16_t)pack2<DT>(real ? v : 0.0f, 0.0f);
+    for (int j = 0; j < 4; ++j) {
+      const int m = rt.m0 + 16 * i + 4 * g + j;
+      if (m >= rt.m1 || c >= a.n) continue;
+      const float v = GATED ? gate(s[0][j], s[HALVES - 1][j]) : s[0][j];
+      const bool real = !rt.zero && source_row(a, m) >= 0;
+      *reinterpret_cast<uint16_t*>(a.y + 2 * (m * a.ldy + c)) = (uint16_t)pack2<DT>(real ? v : 0.0f, 0.0f);
+    }
   }
 }
 

@@ -139,6 +139,20 @@ def test_linear_many_rows_and_columns(qa, fmt, dtype, m, n, k, gated):
 
 
 @pytest.mark.parametrize("fmt", sorted(GROUP))
+@pytest.mark.parametrize("dtype,gated", [("fp16", True), ("bf16", False)])
+@pytest.mark.parametrize("m,n,k", [(12, 12300, 1160), (9, 12300, 1165), (5, 66000, 264), (5, 66000, 259), (30, 66000, 72),
+                                   (30, 66000, 71), (20, 9000, 1288), (100, 2600, 1031), (3, 700, 4136), (7, 333, 2049)])
+def test_linear_few_rows_many_columns(qa, fmt, dtype, gated, m, n, k):
+    if gated:
+        n = (n + 1) // 2
+    wide = n * (2 if gated else 1)
+    p = random_packed(fmt, wide, k, seed=m)
+    x = activations(m, k, dtype, seed=n)
+    y = qa.qr_linear(fmt, x, torch.from_numpy(p.reshape(-1)).cuda(), n, gated=gated)
+    check_product(y, x, weight64(fmt, p, wide, k, dtype), n, gated, dtype, (fmt, dtype, gated, m, n, k))
+
+
+@pytest.mark.parametrize("fmt", sorted(GROUP))
 @pytest.mark.parametrize("dtype", sorted(DT))
 def test_weights_are_the_codec_s(qa, fmt, dtype):
     """A packed weight is qr_encode's, and a unit vector reads out what qr_decode returns."""
@@ -206,18 +220,24 @@ def test_strides_and_alignment(qa, m, k):
         assert (rest == 7.0).all()
 
 
-@pytest.mark.parametrize("m", [5, 40, 300])
-def test_not_finite_values_stay_in_their_row(qa, m):
-    n, k = 64, 333
+@pytest.mark.parametrize("m,n,k", [(5, 64, 333), (40, 64, 333), (300, 64, 333), (5, 66000, 72), (30, 66000, 72), (12, 12300, 600),
+                                   (1300, 4500, 72), (2, 50, 4096)])
+def test_not_finite_values_stay_in_their_row(qa, m, n, k):
     p = random_packed("asym4", n, k, 9)
     w = torch.from_numpy(p.reshape(-1)).cuda()
     x = activations(m, k, "bf16", 2)
     clean = qa.qr_linear("asym4", x, w, n)
-    x[1, 17], x[3, k - 1] = float("nan"), float("inf")
+    x[1, 17], x[m // 3 * 2, k - 1] = float("nan"), float("inf")
     y = qa.qr_linear("asym4", x, w, n)
-    keep = [i for i in range(m) if i not in (1, 3)]
+    keep = [i for i in range(m) if i not in (1, m // 3 * 2)]
     assert torch.equal(y[keep], clean[keep])
-    assert y[1].isnan().all() and not y[3].isfinite().any()
+    assert y[1].isnan().all()
+    if m < 3:
+        return
+    # infinity times each weight that is not zero
+    last = torch.from_numpy(weight64("asym4", p, n, k, "bf16")[0][:, k - 1]).cuda()
+    row = y[m // 3 * 2]
+    assert (row[last > 0] == float("inf")).all() and (row[last < 0] == float("-inf")).all() and row[last == 0].isnan().all()
 
 
 # ---------------------------------------------------------------------------
@@ -264,6 +284,16 @@ def test_experts_many_rows(qa, fmt):
     check_experts(qa, fmt, "fp16", False, [700, 0, 1, 513, 256], 1001, 333, 300, True, seed=4)
     check_experts(qa, fmt, "bf16", True, [700, 0, 1, 513, 256], 2500, 88, 300, True, seed=5)
     check_experts(qa, fmt, "fp16", False, [700, 0, 1, 513, 256], 5003, 104, 300, False, seed=6)
+
+
+@pytest.mark.parametrize("fmt", sorted(GROUP))
+@pytest.mark.parametrize("gated", [False, True])
+def test_experts_many_small_groups(qa, fmt, gated):
+    rng = np.random.default_rng(7)
+    sizes = [int(v) for v in rng.poisson(8, 64)]
+    check_experts(qa, fmt, "bf16", gated, sizes, 1100, 136, 5, True, seed=7)
+    check_experts(qa, fmt, "fp16", gated, [3 * v for v in sizes[:40]], 2601, 77, 9, True, seed=8)
+    check_experts(qa, fmt, "fp16", gated, [20, 0, 31, 5], 700, 1033, 0, False, seed=9)
 
 
 def test_experts_all_rows_dropped(qa):

@@ -10,6 +10,7 @@ import functools
 
 import torch
 
+from . import qr as _qr
 from .qr import DTYPES, _check, _fmt, _ptr, _stream, lib, qr_encode
 
 WEIGHT_FORMATS = {4: 32, 20: 128, 36: 32}   # format id -> values that share a scale
@@ -21,7 +22,7 @@ _bound = None
 def _lib():
     """``libqr.so`` with the signatures of the operators."""
     global _bound
-    if _bound is None or _bound is not lib():
+    if _bound is None or _bound is not _qr._lib:
         L = lib()
         vp, sz, i = ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int
         L.qr_weight_bytes.restype = sz
@@ -100,14 +101,18 @@ def _matrix(t, name, rows, cols, device, dtype):
         raise ValueError(f"{name} is {t.dtype}, the call's dtype is {dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} is {tuple(t.shape)}, the call needs {(rows, cols)}")
+    return t.data_ptr(), _row_stride(t, name, rows, cols)
+
+
+def _row_stride(t, name, rows, cols):
     ld, step = t.stride()
     if step != 1 and cols > 1:
         raise ValueError(f"the values of a row of {name} must be neighbours")
     if rows < 2:
-        ld = cols
-    elif ld < cols:
+        return cols
+    if ld < cols:
         raise ValueError(f"the rows of {name} must not overlap")
-    return t.data_ptr(), ld
+    return ld
 
 
 def _vector(t, name, numel, dtype, device):
@@ -122,13 +127,13 @@ def _vector(t, name, numel, dtype, device):
 def _product_weight(fmt, experts, n, k, gated):
     """Format id and packed bytes of a product's weight."""
     fid = _fmt(fmt)
-    if fid not in WEIGHT_FORMATS or n < 1 or k < 1 or experts < 1:
+    if fid not in WEIGHT_FORMATS or n != int(n) or n < 1 or k < 1 or experts < 1:
         raise ValueError(f"no product of format {fmt!r} with n={n}, k={k}, {experts} expert(s)")
     return fid, _weight_bytes(fid, experts * n * (2 if gated else 1), k)
 
 
 def _product(fn, fmt, x, w, n, gated, y, offsets, rows, stream):
-    if not (isinstance(x, torch.Tensor) and x.dim() == 2):
+    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
         raise ValueError("x must be a device matrix")
     dtype = x.dtype
     dt = DTYPES.get(dtype)
@@ -136,23 +141,22 @@ def _product(fn, fmt, x, w, n, gated, y, offsets, rows, stream):
         raise ValueError(f"unsupported dtype {dtype}")
     tokens, k = x.shape
     dev = x.get_device()
-    n, gated = int(n), bool(gated)
     experts = 1 if offsets is None else offsets.numel() - 1
     fid, nbytes = _product_weight(fmt, experts, n, k, gated)
-    xp, ldx = _matrix(x, "x", tokens, k, dev, dtype)
+    ldx = _row_stride(x, "x", tokens, k)
     wp = _ptr(w, "w", nbytes, dev)
     slots = tokens if rows is None else rows.numel()
     if y is None:
-        y = _empty(x, (slots, n), dtype, stream)
+        y = x.new_empty((slots, n)) if stream is None else _empty(x, (slots, n), dtype, stream)
         yp, ldy = y.data_ptr(), n
     else:
         yp, ldy = _matrix(y, "y", slots, n, dev, dtype)
     if offsets is None:
-        st = _lib().qr_linear(fid, dt, gated, xp, ldx, wp, yp, ldy, slots, n, k, _stream(stream, dev))
+        st = _lib().qr_linear(fid, dt, gated, x.data_ptr(), ldx, wp, yp, ldy, slots, n, k, _stream(stream, dev))
     else:
         op = _vector(offsets, "offsets", experts + 1, torch.int32, dev)
         rp = None if rows is None else _vector(rows, "rows", slots, torch.int32, dev)
-        st = _lib().qr_experts(fid, dt, gated, xp, ldx, tokens, wp, op, rp, yp, ldy, slots, experts, n, k,
+        st = _lib().qr_experts(fid, dt, gated, x.data_ptr(), ldx, tokens, wp, op, rp, yp, ldy, slots, experts, n, k,
                                _stream(stream, dev))
     if st:
         _check(fn, st)
@@ -224,8 +228,10 @@ def _route_workspace(tokens, top, experts):
 def qr_combine(y, pos, gates, out=None, stream=None):
     """out[t] = sum over j of gates[t, j] * y[pos[t, j]] (a position outside y: no term);
     ``pos`` int32 and ``gates`` fp32 are [tokens, top], ``y`` [slots, n]."""
-    if not (isinstance(y, torch.Tensor) and y.dim() == 2 and isinstance(pos, torch.Tensor) and pos.dim() == 2):
-        raise ValueError("y and pos must be device matrices")
+    if not (isinstance(y, torch.Tensor) and y.is_cuda and y.dim() == 2):
+        raise ValueError("y must be a device matrix")
+    if not (isinstance(pos, torch.Tensor) and pos.dim() == 2):
+        raise ValueError("pos must be a device matrix")
     dtype = y.dtype
     dt = DTYPES.get(dtype)
     if dt is None:
@@ -233,9 +239,9 @@ def qr_combine(y, pos, gates, out=None, stream=None):
     slots, n = y.shape
     tokens, top = pos.shape
     dev = y.get_device()
-    yp, ldy = _matrix(y, "y", slots, n, dev, dtype)
+    yp, ldy = y.data_ptr(), _row_stride(y, "y", slots, n)
     if out is None:
-        out = _empty(y, (tokens, n), dtype, stream)
+        out = y.new_empty((tokens, n)) if stream is None else _empty(y, (tokens, n), dtype, stream)
         op, ldo = out.data_ptr(), n
     else:
         op, ldo = _matrix(out, "out", tokens, n, dev, dtype)

@@ -48,8 +48,10 @@ static qr_status launch_few_rows(int rows, const ProductArgs& a, hipStream_t st)
   if (rows > 16 && quads > 256) {
     // two fragments of rows share a weight's decode: 64 experts with 25 rows
     // each 55 us instead of 74, 100 rows of 4096 x 4096 17 instead of 22; with
-    // 8 rows an expert 52 instead of 46
-    if (quads >= 2048) return launch_few<F, DT, GATED, 2, 8, 1, ALIGNED>(a, st);
+    // 8 rows an expert 52 instead of 46.  Two waves share the k axis where
+    // there are few workgroups: 64 rows of 8192 x 8192 32 and 50 us, of 16384 x
+    // 4096 33 and 31
+    if (quads >= 600) return launch_few<F, DT, GATED, 2, 8, 1, ALIGNED>(a, st);
     return launch_few<F, DT, GATED, 2, 4, 2, ALIGNED>(a, st);
   }
   // As many waves share the k axis as it takes to have 4096 waves in all:
@@ -80,9 +82,11 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   // directly, by 32-bit offsets
   const bool aligned = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0 && a.k % 8 == 0 && a.xrows * a.ldx < (1LL << 31);
   const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, 64) * ((a.n * (GATED ? 2LL : 1LL) + 127) / 128);
-  // Few rows, or so few tiles of 64 x 128 that they would leave most CUs idle:
-  // 64 rows of 8192 x 8192 32 us here, 74 tiled; 300 rows of 4096 x 4096 50 and 41
-  if (rows <= 32 || (rows <= 128 && tiles < 128))
+  // Few rows, or so few tiles of 64 x 128 that most CUs would be idle: 64 rows
+  // of 8192 x 8192 32 us here and 74 tiled, 40 experts with 50 rows of 1024 x
+  // 2048 38 and 47, 600 rows of 1024 x 4096 27 and 40; 300 rows of 4096 x 4096
+  // 46 and 42
+  if (rows <= 64 || tiles < 128)
     return aligned ? launch_few_rows<F, DT, GATED, true>(rows, a, st) : launch_few_rows<F, DT, GATED, false>(rows, a, st);
   if (!aligned) return launch_many<F, DT, GATED, 4, 2, 1, false>(a, st);
   const long long large = row_tiles(a.slots, a.experts, !a.offsets, 128) * ((a.n * (GATED ? 2LL : 1LL) + 255) / 256);

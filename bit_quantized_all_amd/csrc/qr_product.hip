@@ -37,7 +37,7 @@ static qr_status launch_rows(const ProductArgs& a, hipStream_t st) {
 
 template <int F, int DT, bool GATED, int MF, int NW, int KW, bool ALIGNED>
 static qr_status launch_few(const ProductArgs& a, hipStream_t st) {
-  return launch_tiles(few_rows_kernel<F, DT, GATED, MF, NW, KW, 1, ALIGNED>, a, 16 * MF, 16 * NW / (GATED ? 2 : 1),
+  return launch_tiles(few_rows_kernel<F, DT, GATED, MF, NW, KW, ALIGNED>, a, 16 * MF, 16 * NW / (GATED ? 2 : 1),
                       kWave * NW * KW, st);
 }
 

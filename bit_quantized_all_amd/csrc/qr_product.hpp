@@ -471,21 +471,21 @@ __device__ __forceinline__ uint32_t lds_address(void* lds) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
 }
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(lds), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
 }
 // One value of SIZE bytes (1 or 2, zero-extended) from each lane's address to lds + 4 lane.
 template <int SIZE>
 __device__ __forceinline__ void load_value_to_lds(const uint8_t* p, uint32_t lds) {
   if constexpr (SIZE == 2)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(lds), "v"(p) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(lds), "v"(p) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
 }
 // The same from a base of the whole wave plus each lane's offset.
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
-               : "s"(lds), "v"(offset), "s"(base)
+               : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
                : "memory");
 }
 // A barrier of the workgroup that leaves loads to LDS on their way, which
@@ -573,7 +573,7 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 // 64-byte piece it touches, 16 when four neighbouring lanes share one and 64
 // when each lane reads a row of its own, as the fragments of the matrix unit
 // want it.  So nothing is loaded in fragment order: codes, scales and x go to
-// LDS in whole runs of a row, DEPTH segments ahead.  There, 16-byte piece p of
+// LDS in whole runs of a row, the next segment's while one is multiplied.  There, 16-byte piece p of
 // row r (a block of codes, a unit of x) lies at place p ^ (r & 7), so that lanes
 // which read one piece of eight rows hit eight different groups of banks; the
 // lanes that load it take their pieces in that order.
@@ -592,14 +592,12 @@ constexpr int kSegment = 256;
 constexpr int kSegBlocks = kSegment / kBlockValues;
 constexpr int kSegUnits = kSegment / 8;
 
-template <int F, int DT, int MF, int NW, int KW, int DEPTH, bool ALIGNED>
+template <int F, int DT, int MF, int NW, int KW, bool ALIGNED>
 struct FewRows {
   static constexpr bool kAsym = Format<F>::kAsym;
   static constexpr bool kZeros = !Format<F>::kFp4;  // codes have a zero point
   static constexpr int XL = MF * 8 / NW;            // loads of x of one wave in a segment: two rows each
   static_assert(XL * NW == MF * 8, "the waves of a group share the loads of x evenly");
-  static constexpr int kLoads = XL + 4;             // loads of one wave in a segment
-  static constexpr int BUF = DEPTH + 1;
   struct Wave {
     u32x4 codes[16][kSegBlocks];
     uint32_t scales[16][kSegBlocks];  // asymmetric: [row][group] scales and, 64 words on, zero points
@@ -609,7 +607,7 @@ struct FewRows {
     Wave w[KW][NW];
   };
   union Stage {
-    Buffer buffer[BUF];
+    Buffer buffer[2];
     f32x4 sums[KW][NW][MF][kWave];  // when all is multiplied
   };
 
@@ -625,7 +623,8 @@ struct FewRows {
     return (lane & 31) ^ ((2 * (nw + NW * t) + (lane >> 5)) & 7);
   }
 
-  __device__ __forceinline__ void fetch(const ProductArgs& a, Buffer& to, int seg, int kw, int nw, int lane) {
+  __device__ __forceinline__ void fetch_weights(const ProductArgs& a, Buffer& to, int seg, int kw, int nw,
+                                                int lane) const {
     constexpr uint32_t TB = Format<F>::kTileBytes;
     const int last = a.blocks - 1;
     // a block past the row's last: that block again, times zeros of x
@@ -649,6 +648,9 @@ struct FewRows {
         load_value_to_lds<2>(w + ((b >> 6) * TB + Format<F>::kScaleOffset + (b & 63) * 2), scales + 256 * q);
       }
     }
+  }
+
+  __device__ __forceinline__ void fetch_x(const ProductArgs& a, Buffer& to, int seg, int kw, int nw, int lane) {
     const bool whole = kSegment * (seg + 1) <= a.k;
     if constexpr (ALIGNED) {
       const uint8_t* from = a.x + 2 * kSegment * (size_t)seg;
@@ -681,7 +683,16 @@ struct FewRows {
     }
   }
 
-  // Adds this wave's share to acc.
+  // Asks for the first segment.  Its weights need not wait for the numbers of the
+  // rows of x, which are a trip to memory of their own.
+  template <typename ROWS>
+  __device__ __forceinline__ void begin(const ProductArgs& a, Stage& stage, int kw, int nw, int lane, ROWS find) {
+    if (kSegment * kw < a.k) fetch_weights(a, stage.buffer[0], kw, kw, nw, lane);
+    find();
+    if (kSegment * kw < a.k) fetch_x(a, stage.buffer[0], kw, kw, nw, lane);
+  }
+
+  // Adds this wave's share to acc, after begin().
   template <bool SIGNED>
   __device__ __forceinline__ void sum(const ProductArgs& a, Stage& stage, int kw, int nw, int lane) {
     const int r = lane & 15, g = lane >> 4;
@@ -693,18 +704,11 @@ struct FewRows {
                                   : (DT == kFp16 ? 0xC800C800u : 0xC100C100u);  // -8
     const u32x4 factors = {factor, factor, factor, factor};
     const int segments = (a.k + kSegment - 1) / kSegment;  // each has values of x
-    constexpr int ahead = ALIGNED ? DEPTH : 1;
-#pragma unroll
-    for (int d = 0; d < ahead; ++d)
-      if (d * KW + kw < segments) fetch(a, stage.buffer[d], d * KW + kw, kw, nw, lane);
     // every wave goes through as many rounds as the first group
-    for (int s0 = 0, buf = 0; s0 < segments; s0 += KW, buf = buf + 1 == BUF ? 0 : buf + 1) {
+    for (int s0 = 0, buf = 0; s0 < segments; s0 += KW, buf = buf ? 0 : 1) {
       const int seg = s0 + kw;
       Buffer& now = stage.buffer[buf];
-      if (ahead == 2 && seg + KW < segments)
-        loads_done<kLoads>();
-      else
-        loads_done<0>();
+      loads_done<0>();
       if constexpr (!ALIGNED) {
         if (seg < segments) {
 #pragma unroll
@@ -712,8 +716,10 @@ struct FewRows {
         }
       }
       stage_barrier();
-      const int next = buf + ahead >= BUF ? buf + ahead - BUF : buf + ahead;
-      if (seg + ahead * KW < segments) fetch(a, stage.buffer[next], seg + ahead * KW, kw, nw, lane);
+      if (seg + KW < segments) {
+        fetch_weights(a, stage.buffer[1 - buf], seg + KW, kw, nw, lane);
+        fetch_x(a, stage.buffer[1 - buf], seg + KW, kw, nw, lane);
+      }
       if (seg >= segments) continue;
       const Wave& mine = now.w[kw][nw];
       u32x4 codes[2];
@@ -771,9 +777,9 @@ struct FewRows {
   }
 };
 
-template <int F, int DT, bool GATED, int MF, int NW, int KW, int DEPTH, bool ALIGNED>
+template <int F, int DT, bool GATED, int MF, int NW, int KW, bool ALIGNED>
 __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) {
-  using T = FewRows<F, DT, MF, NW, KW, DEPTH, ALIGNED>;
+  using T = FewRows<F, DT, MF, NW, KW, ALIGNED>;
   constexpr int HALVES = GATED ? 2 : 1;
   constexpr int NF = NW / HALVES;  // column fragments of y
   __shared__ typename T::Stage stage;
@@ -789,17 +795,6 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 
   if (!rt.zero) {
     T t;
-#pragma unroll
-    for (int i = 0; i < T::XL; ++i) {
-      // rows past the end repeat the last, rows of no source the first of x
-      const int m = rt.m0 + 2 * (nw + NW * i) + (lane >> 5);
-      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
-      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * T::unit_of(lane, i, nw);
-      if constexpr (ALIGNED)
-        t.xoff[i] = (uint32_t)at;
-      else
-        t.xrow[i] = a.x + at;
-    }
     const int c0 = n0 + 16 * (nw % NF);  // first weight row of the wave, of the gate or the up rows
     const long long row0 = ((long long)rt.expert * HALVES + nw / NF) * a.n;
     const long long first = (row0 + n0) * a.blocks;
@@ -811,6 +806,19 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 #pragma unroll
     for (int q = 0; q < 2; ++q) t.cblock[q] = block_of(c0 + 8 * q + (lane >> 3));
     t.gblock = block_of(c0 + (lane >> 1) % 16);
+    t.begin(a, stage, kw, nw, lane, [&] {
+#pragma unroll
+      for (int i = 0; i < T::XL; ++i) {
+        // rows past the end repeat the last, rows of no source the first of x
+        const int m = rt.m0 + 2 * (nw + NW * i) + (lane >> 5);
+        const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
+        const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * T::unit_of(lane, i, nw);
+        if constexpr (ALIGNED)
+          t.xoff[i] = (uint32_t)at;
+        else
+          t.xrow[i] = a.x + at;
+      }
+    });
     t.template sum<false>(a, stage, kw, nw, lane);
     if constexpr (T::kZeros) {
       bool finite = true;
@@ -823,6 +831,7 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
         f32x4 was[MF];
 #pragma unroll
         for (int i = 0; i < MF; ++i) was[i] = t.acc[i];
+        t.begin(a, stage, kw, nw, lane, [] {});
         t.template sum<true>(a, stage, kw, nw, lane);
         // the finite ones stay as they are, so that no row depends on another
 #pragma unroll
@@ -947,22 +956,6 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     for (int f = 0; f < NFR; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   if (!rt.zero) {
-    // x: load i of this wave brings rows 8 (XI wave + i) + lane / 8 of the tile,
-    // unit (lane & 7) ^ (row & 7); rows past the end repeat the last, rows of no
-    // source the first of x
-    const int unit = (lane & 7) ^ (lane >> 3);
-    const uint8_t* xrow[ALIGNED ? 1 : XI];
-    uint32_t xoff[XI];
-#pragma unroll
-    for (int i = 0; i < XI; ++i) {
-      const int m = rt.m0 + 8 * (XI * wave + i) + (lane >> 3);
-      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
-      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * unit;
-      if constexpr (ALIGNED)
-        xoff[i] = (uint32_t)at;
-      else
-        xrow[i] = a.x + at;
-    }
     // weights: row R of the tile is a column of its half; columns past the last repeat it
     const long long row0 = (long long)rt.expert * HALVES * a.n;
     // load l of this wave brings rows 32 (WAVES l + wave) + lane / 2, block lane & 1
@@ -980,6 +973,12 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       wfirst[l] = (uint32_t)(block & 63);
     }
 
+    // x: load i of this wave brings rows 8 (XI wave + i) + lane / 8 of the tile,
+    // unit (lane & 7) ^ (row & 7); rows past the end repeat the last, rows of no
+    // source the first of x
+    const int unit = (lane & 7) ^ (lane >> 3);
+    const uint8_t* xrow[ALIGNED ? 1 : XI];
+    uint32_t xoff[XI];
     const int last = a.blocks - 1;
     const int stages = (a.k + kStage - 1) / kStage;  // each has values of x
     u32x4 xv[ALIGNED ? 1 : XI];
@@ -1037,11 +1036,24 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       return decode_unit<F, DT>(code[f], BlockScale<F, DT>(raw));
     };
 
-    // the first DEPTH stages of x, and one more of weights
+    // The first DEPTH stages of x, and one more of weights.  The first weights
+    // need not wait for the numbers of the rows of x, which are a trip to memory
+    // of their own.
     fetch_weights(0, 0);
+    fetch_weights(1, 1);
+#pragma unroll
+    for (int i = 0; i < XI; ++i) {
+      const int m = rt.m0 + 8 * (XI * wave + i) + (lane >> 3);
+      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
+      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * unit;
+      if constexpr (ALIGNED)
+        xoff[i] = (uint32_t)at;
+      else
+        xrow[i] = a.x + at;
+    }
 #pragma unroll
     for (int d = 0; d < (ALIGNED ? DEPTH : 1); ++d) {
-      fetch_weights(1 + d, 1 + d);
+      if (d > 0) fetch_weights(1 + d, 1 + d);
 #pragma unroll
       for (int i = 0; i < XI; ++i) fetch_x(d < stages ? d : stages - 1, d, i);
     }

@@ -488,6 +488,19 @@ __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
                : "memory");
 }
+template <int SIZE>
+__device__ __forceinline__ void load_value_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
+  if constexpr (SIZE == 2)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
+                 : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2"
+                 :
+                 : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
+                 : "memory");
+}
 // A barrier of the workgroup that leaves loads to LDS on their way, which
 // __syncthreads() would wait for; each wave's LDS accesses are done before it.
 __device__ __forceinline__ void stage_barrier() {
@@ -918,24 +931,26 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
   constexpr int BM = 16 * WM * MFR, BN = 16 * WN * NFR;
   constexpr int COLS = 16 * NFR / HALVES;         // columns of y of one wave
   constexpr int XI = BM / 8 / WAVES;              // loads of x of one wave in a stage: 8 rows each
-  constexpr int WI = BN / 32;                     // loads of codes of the workgroup: 32 rows each
   static_assert(XI * 8 * WAVES == BM, "the waves share the loads of x evenly");
-  constexpr int WL = (WI + WAVES - 1) / WAVES;    // ... of one wave
+  constexpr int WL = BN / 16 / WAVES;             // loads of codes of one wave in a chunk: a fragment's rows each
+  static_assert(WL * 16 * WAVES == BN && WL <= MFR, "the waves share the loads of codes evenly");
   static_assert(XI <= MFR, "a load of x goes with each row of the first step's products");
   static_assert(MFR % NFR == 0, "one fragment is decoded every MFR / NFR rows of products");
   constexpr uint32_t TB = Format<F>::kTileBytes;
   constexpr bool kAsym = Format<F>::kAsym;
-  // codes and scales come a stage earlier than x: the first step of a stage is
-  // decoded while the last of the one before it is multiplied
   struct Weights {
-    u32x4 codes[BN][kStageBlocks];
-    uint32_t scales[BN][kStageBlocks];              // of both blocks; the group's, twice
-    uint32_t zeros[kAsym ? BN : 1][kStageBlocks];
+    u32x4 codes[BN][kChunkBlocks];
+    uint32_t scales[BN][kChunkBlocks];              // asymmetric: the group's, four times
+    uint32_t zeros[kAsym ? BN : 1][kChunkBlocks];
   };
-  // loads of one stage of one wave
-  constexpr int kLoads = XI + WL * (kAsym ? 3 : 2);
-  static_assert(WI % WAVES == 0, "every wave has as many loads");
-  constexpr int XBUF = DEPTH + 1, WBUF = DEPTH + 2;
+  constexpr int kWeightLoads = WL * (kAsym ? 3 : 2);  // of one wave in a chunk
+  constexpr int XBUF = DEPTH + 1, WBUF = DEPTH + 1;
+  // The first step of a chunk is decoded while the last of the one before it is
+  // multiplied, so a chunk is in LDS by the second stage of that one, and its
+  // place is free from the first.  A stage waits for what the DEPTH - 1 before it
+  // did not ask for: with DEPTH 2, weights are asked for in the second stage.
+  static_assert(DEPTH == 1 || DEPTH == 2, "the waits below");
+  constexpr int kWeightStage = DEPTH - 1;
   __shared__ u32x4 lds_x[XBUF][BM][8];
   __shared__ Weights lds_w[WBUF];
 
@@ -956,21 +971,19 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     for (int f = 0; f < NFR; ++f) acc[i][f] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
   if (!rt.zero) {
-    // weights: row R of the tile is a column of its half; columns past the last repeat it
-    const long long row0 = (long long)rt.expert * HALVES * a.n;
-    // load l of this wave brings rows 32 (WAVES l + wave) + lane / 2, block lane & 1
-    const uint8_t* wlane[WL];
-    uint32_t wfirst[WL];
+    // weights: row R of the tile is a column of its half; columns past the last
+    // repeat it.  Load l of this wave brings fragment WAVES l + wave, row lane / 4
+    const long long row0 = (long long)rt.expert * HALVES * a.n + n0;
+    const uint8_t* wbase[WL];
+    uint32_t wblock[WL];  // first block of the lane's row, from wbase
 #pragma unroll
     for (int l = 0; l < WL; ++l) {
-      const int R = 32 * (WAVES * l + wave) + (lane >> 1);
-      const int f = R / 16 % NFR, q = R & 15;
+      const int part = WAVES * l + wave, f = part % NFR, q = lane >> 2;
       const int half = f / OUT, ff = f % OUT;
-      const int in = PAIR == 2 ? 32 * (ff >> 1) + 8 * (q >> 2) + 4 * (ff & 1) + (q & 3) : q;
-      const int c = n0 + COLS * (R / (16 * NFR)) + in;
-      const long long block = (row0 + (long long)half * a.n + (c < a.n ? c : a.n - 1)) * a.blocks;
-      wlane[l] = a.w + (block >> 6) * TB;
-      wfirst[l] = (uint32_t)(block & 63);
+      const int in = COLS * (part / NFR) + (PAIR == 2 ? 32 * (ff >> 1) + 8 * (q >> 2) + 4 * (ff & 1) + (q & 3) : q);
+      const long long first = (row0 + (long long)half * a.n) * a.blocks;
+      wbase[l] = a.w + (first >> 6) * TB;
+      wblock[l] = (uint32_t)(first & 63) + (uint32_t)(n0 + in < a.n ? in : a.n - 1 - n0) * (uint32_t)a.blocks;
     }
 
     // x: load i of this wave brings rows 8 (XI wave + i) + lane / 8 of the tile,
@@ -982,21 +995,18 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     const int last = a.blocks - 1;
     const int stages = (a.k + kStage - 1) / kStage;  // each has values of x
     u32x4 xv[ALIGNED ? 1 : XI];
-    auto fetch_weights = [&](int st, int buf) {
-      const int kb = st * kStageBlocks + (lane & 1);
-      const uint32_t kc = (uint32_t)(kb < last ? kb : last);  // past the last: that one, times zeros of x
-      const uint32_t to = (uint32_t)(sizeof(Weights) * buf);
-#pragma unroll
-      for (int l = 0; l < WL; ++l) {
-        const int part = WAVES * l + wave;
-        const uint32_t b = wfirst[l] + kc, at = (b >> 6) * TB, in = b & 63;
-        load_to_lds(wlane[l] + (at + in * 16), lds_address(&lds_w[0].codes[0][0]) + to + (uint32_t)(1024 * part));
-        load_value_to_lds<2>(wlane[l] + (at + Format<F>::kScaleOffset + (kAsym ? in >> 2 : in) * 2),
-                             lds_address(&lds_w[0].scales[0][0]) + to + (uint32_t)(256 * part));
-        if constexpr (kAsym)
-          load_value_to_lds<1>(wlane[l] + (at + Format<F>::kZeroOffset + (in >> 2)),
-                               lds_address(&lds_w[0].zeros[0][0]) + to + (uint32_t)(256 * part));
-      }
+    auto fetch_weights = [&](int chunk, int buf, int l) {
+      const int kb = chunk * kChunkBlocks + ((lane & 3) ^ (lane >> 4));
+      // past the last: that one, times zeros of x
+      const uint32_t b = wblock[l] + (uint32_t)(kb < last ? kb : last), at = (b >> 6) * TB, in = b & 63;
+      const uint32_t to = lds_address(&lds_w[0]) + (uint32_t)(sizeof(Weights) * buf);
+      const int part = WAVES * l + wave;
+      load_to_lds(wbase[l], at + in * 16, to + (uint32_t)(1024 * part));
+      load_value_to_lds<2>(wbase[l], at + Format<F>::kScaleOffset + (kAsym ? in >> 2 : in) * 2,
+                           to + (uint32_t)(offsetof(Weights, scales) + 256 * part));
+      if constexpr (kAsym)
+        load_value_to_lds<1>(wbase[l], at + Format<F>::kZeroOffset + (in >> 2),
+                             to + (uint32_t)(offsetof(Weights, zeros) + 256 * part));
     };
     // Rows that begin on 16 bytes (ALIGNED) go to LDS directly, and where a row
     // ends, zeros instead; others pass through registers.
@@ -1020,13 +1030,14 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     };
     u32x4 wv[NFR];
     uint32_t code[NFR], scale[NFR], zero[NFR];
+    // codes and scales of block b of a chunk
     auto read_step = [&](const Weights& w, int b) {
 #pragma unroll
       for (int f = 0; f < NFR; ++f) {
-        const int R = 16 * (NFR * wn + f) + r;
-        code[f] = reinterpret_cast<const uint32_t*>(&w.codes[R][b])[g];
-        scale[f] = w.scales[R][b];
-        zero[f] = kAsym ? w.zeros[kAsym ? R : 0][b] : 0u;
+        const int R = 16 * (NFR * wn + f) + r, p = b ^ (r >> 2);
+        code[f] = reinterpret_cast<const uint32_t*>(&w.codes[R][p])[g];
+        scale[f] = w.scales[R][p];
+        zero[f] = kAsym ? w.zeros[kAsym ? R : 0][p] : 0u;
       }
     };
     auto decode = [&](int f) {
@@ -1036,11 +1047,11 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       return decode_unit<F, DT>(code[f], BlockScale<F, DT>(raw));
     };
 
-    // The first DEPTH stages of x, and one more of weights.  The first weights
-    // need not wait for the numbers of the rows of x, which are a trip to memory
-    // of their own.
-    fetch_weights(0, 0);
-    fetch_weights(1, 1);
+    // The first DEPTH stages of x and chunks of weights.  The first weights need
+    // not wait for the numbers of the rows of x, which are a trip to memory of
+    // their own.
+#pragma unroll
+    for (int l = 0; l < WL; ++l) fetch_weights(0, 0, l);
 #pragma unroll
     for (int i = 0; i < XI; ++i) {
       const int m = rt.m0 + 8 * (XI * wave + i) + (lane >> 3);
@@ -1052,14 +1063,24 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
         xrow[i] = a.x + at;
     }
 #pragma unroll
-    for (int d = 0; d < (ALIGNED ? DEPTH : 1); ++d) {
-      if (d > 0) fetch_weights(1 + d, 1 + d);
+    for (int d = 0; d < DEPTH; ++d) {
+      if (d > 0) {
+#pragma unroll
+        for (int l = 0; l < WL; ++l) fetch_weights(d, d, l);
+      }
 #pragma unroll
       for (int i = 0; i < XI; ++i) fetch_x(d < stages ? d : stages - 1, d, i);
     }
-    for (int st = 0, xb = 0, wb = 0; st < stages; ++st) {  // xb, wb: where stage st's x and weights are
+    // xb, wb: where the x of the stage and the weights of its chunk are
+    for (int st = 0, xb = 0, wb = 0; st < stages; ++st) {
+      const int h = st & 1;  // stage of the chunk
+      const int wn1 = wb + 1 == WBUF ? 0 : wb + 1;
+      const int wnew = wb + DEPTH >= WBUF ? wb + DEPTH - WBUF : wb + DEPTH;
       if constexpr (ALIGNED) {
-        loads_done<(DEPTH - 1) * kLoads>();
+        if (h == kWeightStage)
+          loads_done<(DEPTH - 1) * XI>();
+        else
+          loads_done<(DEPTH - 1) * (XI + kWeightLoads)>();
       } else {
         loads_done<0>();
 #pragma unroll
@@ -1071,18 +1092,23 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
 #pragma unroll
         for (int f = 0; f < NFR; ++f) wv[f] = decode(f);
       }
-      constexpr int ahead = ALIGNED ? DEPTH : 1;
-      const int xn = xb + ahead >= XBUF ? xb + ahead - XBUF : xb + ahead;
-      const int wn1 = wb + 1 == WBUF ? 0 : wb + 1;
-      const int wna = wb + 1 + ahead >= WBUF ? wb + 1 + ahead - WBUF : wb + 1 + ahead;
+      // past the last: loads that nobody reads, so that each stage has as many
+      if (h == kWeightStage) {
+#pragma unroll
+        for (int l = 0; l < WL; ++l) fetch_weights((st >> 1) + DEPTH, wnew, l);
+      }
+      const int xn = xb + DEPTH >= XBUF ? xb + DEPTH - XBUF : xb + DEPTH;
       const u32x4(*xs)[8] = &lds_x[xb][16 * MFR * wm + r];
 #pragma unroll
       for (int b = 0; b < kStageBlocks; ++b) {
         // This step's products, with the next step's decode and the next
-        // stage's loads in between: the matrix unit and the vector unit work
-        // side by side.  The compiler would decode first and multiply then; it
-        // is held to this order.
-        read_step(lds_w[b + 1 < kStageBlocks ? wb : wn1], (b + 1) % kStageBlocks);
+        // loads in between: the matrix unit and the vector unit work side by
+        // side.  The compiler would decode first and multiply then; it is
+        // held to this order.
+        if (b + 1 < kStageBlocks)
+          read_step(lds_w[wb], kStageBlocks * h + b + 1);
+        else
+          read_step(lds_w[h ? wn1 : wb], kStageBlocks * (1 - h));
         u32x4 next[NFR], x[MFR];
 #pragma unroll
         for (int i = 0; i < 2; ++i) x[i] = xs[16 * i][(4 * b + g) ^ (r & 7)];
@@ -1107,15 +1133,13 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
             }
             __builtin_amdgcn_sched_barrier(0);
           }
-          // past the last stage: loads that nobody reads, so that each stage has as many
-          if (b == 0 && i == 0) fetch_weights(st + 1 + ahead, wna);
-          if (b == 0 && i < XI) fetch_x(st + ahead < stages ? st + ahead : stages - 1, xn, i);
+          if (b == 0 && i < XI) fetch_x(st + DEPTH < stages ? st + DEPTH : stages - 1, xn, i);
         }
 #pragma unroll
         for (int f = 0; f < NFR; ++f) wv[f] = next[f];
       }
       xb = xb + 1 == XBUF ? 0 : xb + 1;
-      wb = wn1;
+      wb = h ? wn1 : wb;
     }
     loads_done<0>();  // before the workgroup's LDS goes to another
   }

@@ -65,10 +65,10 @@ static qr_status launch_few_rows(int rows, const ProductArgs& a, hipStream_t st)
   return launch_few<F, DT, GATED, 1, 2, 4, ALIGNED>(a, st);
 }
 
-template <int F, int DT, bool GATED, int MFR, int NFR, int DEPTH, bool ALIGNED>
+template <int F, int DT, bool GATED, int WM, int MFR, int NFR, bool ALIGNED>
 static qr_status launch_many(const ProductArgs& a, hipStream_t st) {
-  return launch_tiles(many_rows_kernel<F, DT, GATED, 1, 4, MFR, NFR, DEPTH, ALIGNED>, a, 16 * MFR,
-                      64 * NFR / (GATED ? 2 : 1), kWave * 4, st);
+  return launch_tiles(many_rows_kernel<F, DT, GATED, WM, 4, MFR, NFR, ALIGNED>, a, 16 * WM * MFR,
+                      64 * NFR / (GATED ? 2 : 1), kWave * 4 * WM, st);
 }
 
 template <int F, int DT, bool GATED>
@@ -88,10 +88,16 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   // 46 and 42
   if (rows <= 64 || tiles < 128)
     return aligned ? launch_few_rows<F, DT, GATED, true>(rows, a, st) : launch_few_rows<F, DT, GATED, false>(rows, a, st);
-  if (!aligned) return launch_many<F, DT, GATED, 4, 2, 1, false>(a, st);
+  if (!aligned) return launch_many<F, DT, GATED, 1, 4, 2, false>(a, st);
   const long long large = row_tiles(a.slots, a.experts, !a.offsets, 128) * ((a.n * (GATED ? 2LL : 1LL) + 255) / 256);
-  if (large >= 192 && (!a.offsets || rows >= 192)) return launch_many<F, DT, GATED, 8, 4, 1, true>(a, st);
-  return launch_many<F, DT, GATED, 4, 2, 2, true>(a, st);
+  if (large >= 192 && (!a.offsets || rows >= 192)) {
+    // Up to one large tile a CU, 8 waves share one, of 256 x 128: each SIMD
+    // then has two waves to alternate between.  1024 rows of 8192 x 8192 148 us
+    // and 174 with 4 waves, 768 rows 127 and 151; 1536 rows 251 and 224
+    if (!a.offsets && large <= 256) return launch_many<F, DT, GATED, 2, 8, 2, true>(a, st);
+    return launch_many<F, DT, GATED, 1, 8, 4, true>(a, st);
+  }
+  return launch_many<F, DT, GATED, 1, 4, 2, true>(a, st);
 }
 
 template <int F>

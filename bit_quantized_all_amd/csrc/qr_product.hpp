@@ -889,8 +889,8 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 
 // A workgroup of WM x WN waves computes a tile of WM MFR 16 rows of x by WN NFR
 // 16 weight rows, each wave MFR x NFR fragments of it, in stages of 64 values
-// of k.  A stage's x, codes and scales go to LDS without a stop in registers,
-// DEPTH stages ahead.  Each wave decodes the weights it multiplies, rounded to
+// of k.  A stage's x and a chunk's codes and scales go to LDS without a stop in
+// registers, while the one before is multiplied.  Each wave decodes the weights it multiplies, rounded to
 // the dtype as qr_decode does, straight into the matrix unit's A: they pass LDS
 // once, in 4 bits, and the work of a decode is shared by MFR products.
 //
@@ -922,7 +922,7 @@ __device__ __forceinline__ TileIndex tile_index(int id, int total, int ncols) {
   return {band * kBand + in % height, in / height};
 }
 
-template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR, int DEPTH, bool ALIGNED>
+template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR, bool ALIGNED>
 __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs a) {
   constexpr int WAVES = WM * WN, HALVES = GATED ? 2 : 1;
   constexpr int OUT = NFR / HALVES;               // column fragments of y of one wave
@@ -943,16 +943,11 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     uint32_t scales[BN][kChunkBlocks];              // asymmetric: the group's, four times
     uint32_t zeros[kAsym ? BN : 1][kChunkBlocks];
   };
-  constexpr int kWeightLoads = WL * (kAsym ? 3 : 2);  // of one wave in a chunk
-  constexpr int XBUF = DEPTH + 1, WBUF = DEPTH + 1;
   // The first step of a chunk is decoded while the last of the one before it is
-  // multiplied, so a chunk is in LDS by the second stage of that one, and its
-  // place is free from the first.  A stage waits for what the DEPTH - 1 before it
-  // did not ask for: with DEPTH 2, weights are asked for in the second stage.
-  static_assert(DEPTH == 1 || DEPTH == 2, "the waits below");
-  constexpr int kWeightStage = DEPTH - 1;
-  __shared__ u32x4 lds_x[XBUF][BM][8];
-  __shared__ Weights lds_w[WBUF];
+  // multiplied: a chunk is asked for in the first stage of the one before it,
+  // and in LDS by its second.
+  __shared__ u32x4 lds_x[2][BM][8];
+  __shared__ Weights lds_w[2];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
@@ -1047,9 +1042,8 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       return decode_unit<F, DT>(code[f], BlockScale<F, DT>(raw));
     };
 
-    // The first DEPTH stages of x and chunks of weights.  The first weights need
-    // not wait for the numbers of the rows of x, which are a trip to memory of
-    // their own.
+    // The first weights need not wait for the numbers of the rows of x, which are
+    // a trip to memory of their own.
 #pragma unroll
     for (int l = 0; l < WL; ++l) fetch_weights(0, 0, l);
 #pragma unroll
@@ -1063,28 +1057,13 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
         xrow[i] = a.x + at;
     }
 #pragma unroll
-    for (int d = 0; d < DEPTH; ++d) {
-      if (d > 0) {
+    for (int i = 0; i < XI; ++i) fetch_x(0, 0, i);
+    for (int st = 0; st < stages; ++st) {
+      const int h = st & 1, wb = (st >> 1) & 1;  // stage of the chunk; where its weights are
+      loads_done<0>();
+      if constexpr (!ALIGNED) {
 #pragma unroll
-        for (int l = 0; l < WL; ++l) fetch_weights(d, d, l);
-      }
-#pragma unroll
-      for (int i = 0; i < XI; ++i) fetch_x(d < stages ? d : stages - 1, d, i);
-    }
-    // xb, wb: where the x of the stage and the weights of its chunk are
-    for (int st = 0, xb = 0, wb = 0; st < stages; ++st) {
-      const int h = st & 1;  // stage of the chunk
-      const int wn1 = wb + 1 == WBUF ? 0 : wb + 1;
-      const int wnew = wb + DEPTH >= WBUF ? wb + DEPTH - WBUF : wb + DEPTH;
-      if constexpr (ALIGNED) {
-        if (h == kWeightStage)
-          loads_done<(DEPTH - 1) * XI>();
-        else
-          loads_done<(DEPTH - 1) * (XI + kWeightLoads)>();
-      } else {
-        loads_done<0>();
-#pragma unroll
-        for (int i = 0; i < XI; ++i) lds_x[xb][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
+        for (int i = 0; i < XI; ++i) lds_x[h][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
       }
       stage_barrier();
       if (st == 0) {
@@ -1092,13 +1071,11 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
 #pragma unroll
         for (int f = 0; f < NFR; ++f) wv[f] = decode(f);
       }
-      // past the last: loads that nobody reads, so that each stage has as many
-      if (h == kWeightStage) {
+      if (h == 0 && st + 2 < stages) {
 #pragma unroll
-        for (int l = 0; l < WL; ++l) fetch_weights((st >> 1) + DEPTH, wnew, l);
+        for (int l = 0; l < WL; ++l) fetch_weights((st >> 1) + 1, 1 - wb, l);
       }
-      const int xn = xb + DEPTH >= XBUF ? xb + DEPTH - XBUF : xb + DEPTH;
-      const u32x4(*xs)[8] = &lds_x[xb][16 * MFR * wm + r];
+      const u32x4(*xs)[8] = &lds_x[h][16 * MFR * wm + r];
 #pragma unroll
       for (int b = 0; b < kStageBlocks; ++b) {
         // This step's products, with the next step's decode and the next
@@ -1108,14 +1085,14 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
         if (b + 1 < kStageBlocks)
           read_step(lds_w[wb], kStageBlocks * h + b + 1);
         else
-          read_step(lds_w[h ? wn1 : wb], kStageBlocks * (1 - h));
+          read_step(lds_w[h ? 1 - wb : wb], kStageBlocks * (1 - h));
         u32x4 next[NFR], x[MFR];
 #pragma unroll
         for (int i = 0; i < 2; ++i) x[i] = xs[16 * i][(4 * b + g) ^ (r & 7)];
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < MFR; ++i) {
-          constexpr int kEvery = MFR / NFR;
+          constexpr int kEvery = MFR / NFR, kPer = (XI + NFR - 1) / NFR;
           if (i + 2 < MFR) x[i + 2] = xs[16 * (i + 2)][(4 * b + g) ^ (r & 7)];
 #pragma unroll
           for (int f = 0; f < NFR; ++f) acc[i][f] = mfma<DT>(wv[f], x[i], acc[i][f]);
@@ -1132,16 +1109,17 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
               }
             }
             __builtin_amdgcn_sched_barrier(0);
+            if (b == 0 && st + 1 < stages) {
+#pragma unroll
+              for (int l = (i / kEvery) * kPer; l < XI && l < (i / kEvery + 1) * kPer; ++l) fetch_x(st + 1, 1 - h, l);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
-          if (b == 0 && i < XI) fetch_x(st + DEPTH < stages ? st + DEPTH : stages - 1, xn, i);
         }
 #pragma unroll
         for (int f = 0; f < NFR; ++f) wv[f] = next[f];
       }
-      xb = xb + 1 == XBUF ? 0 : xb + 1;
-      wb = h ? wn1 : wb;
     }
-    loads_done<0>();  // before the workgroup's LDS goes to another
   }
 
 #pragma unroll

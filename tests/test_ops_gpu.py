@@ -139,6 +139,18 @@ def test_linear_many_rows_and_columns(qa, fmt, dtype, m, n, k, gated):
 
 
 @pytest.mark.parametrize("fmt", sorted(GROUP))
+@pytest.mark.parametrize("dtype,m,n,k,gated", [("bf16", 2050, 4500, 328, False), ("fp16", 4100, 2305, 136, True),
+                                               ("fp16", 2305, 4200, 64, False), ("bf16", 1025, 5003, 456, False)])
+def test_linear_many_tiles(qa, fmt, dtype, m, n, k, gated):
+    """Above and below one large tile a CU; odd and even numbers of stages, whole and not."""
+    wide = n * (2 if gated else 1)
+    p = random_packed(fmt, wide, k, seed=m)
+    x = activations(m, k, dtype, seed=n)
+    y = qa.qr_linear(fmt, x, torch.from_numpy(p.reshape(-1)).cuda(), n, gated=gated)
+    check_product(y, x, weight64(fmt, p, wide, k, dtype), n, gated, dtype, (fmt, dtype, gated, m, n, k))
+
+
+@pytest.mark.parametrize("fmt", sorted(GROUP))
 @pytest.mark.parametrize("dtype,gated", [("fp16", True), ("bf16", False)])
 @pytest.mark.parametrize("m,n,k", [(12, 12300, 1160), (9, 12300, 1165), (5, 66000, 264), (5, 66000, 259), (30, 66000, 72),
                                    (30, 66000, 71), (20, 9000, 1288), (100, 2600, 1031), (3, 700, 4136), (7, 333, 2049)])

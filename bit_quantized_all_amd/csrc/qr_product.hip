@@ -82,13 +82,18 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   // directly, by 32-bit offsets
   const bool aligned = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0 && a.k % 8 == 0 && a.xrows * a.ldx < (1LL << 31);
   const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, 64) * ((a.n * (GATED ? 2LL : 1LL) + 127) / 128);
-  // Few rows, or so few tiles of 64 x 128 that most CUs would be idle: 64 rows
-  // of 8192 x 8192 32 us here and 74 tiled, 40 experts with 50 rows of 1024 x
-  // 2048 38 and 47, 600 rows of 1024 x 4096 27 and 40; 300 rows of 4096 x 4096
-  // 46 and 42
-  if (rows <= 64 || tiles < 128)
+  // Few rows, or no more tiles of 64 x 128 than CUs, which one workgroup of
+  // four waves would not keep busy: 64 rows of 8192 x 8192 32 us here and 85
+  // tiled, 192 rows 76 and 86, 300 rows of 4096 x 4096 40 and 46, 600 of 1024 x
+  // 4096 27 and 45, 40 experts with 50 rows of 1024 x 2048 38 and 41; with twice
+  // as many tiles, 512 rows of 8192 x 8192, 156 and 111
+  if (rows <= 64 || tiles <= 256)
     return aligned ? launch_few_rows<F, DT, GATED, true>(rows, a, st) : launch_few_rows<F, DT, GATED, false>(rows, a, st);
   if (!aligned) return launch_many<F, DT, GATED, 1, 4, 2, false>(a, st);
+  // Tiles of 128 x 256 decode a weight half as often as those of 64 x 128, but
+  // leave more of the last one of a group empty: 16 experts with 330 rows of 2048
+  // x 4096 130 us and 160, 8 with 200 rows of 4096 x 4096 128 both, 64 with 160
+  // of 1024 x 2048 106 and 87
   const long long large = row_tiles(a.slots, a.experts, !a.offsets, 128) * ((a.n * (GATED ? 2LL : 1LL) + 255) / 256);
   if (large >= 192 && (!a.offsets || rows >= 192)) {
     // Up to one large tile a CU, 8 waves share one, of 256 x 128: each SIMD

@@ -252,6 +252,32 @@ def test_not_finite_values_stay_in_their_row(qa, m, n, k):
     assert (row[last > 0] == float("inf")).all() and (row[last < 0] == float("-inf")).all() and row[last == 0].isnan().all()
 
 
+@pytest.mark.parametrize("fmt", sorted(GROUP))
+@pytest.mark.parametrize("dtype,gated", [("fp16", False), ("bf16", True)])
+@pytest.mark.parametrize("k,off", [(200, 0), (136, 8), (203, 0), (71, 1), (64, 3)])
+def test_linear_middle(qa, fmt, dtype, gated, k, off):
+    """More small tiles than CUs, and few large ones; x that may pass to LDS directly and x
+    that may not, as part of a larger matrix, with rows that are not finite."""
+    m, n = 700, 3300 if not gated else 1601
+    wide = n * (2 if gated else 1)
+    p = random_packed(fmt, wide, k, seed=k)
+    w = torch.from_numpy(p.reshape(-1)).cuda()
+    big = torch.full((m, k + 24 + off), float("nan"), dtype=DT[dtype], device="cuda")
+    out = torch.full((m + 2, n + 3), 7.0, dtype=DT[dtype], device="cuda")
+    x, y = big[:, off:off + k], out[1:-1, 1:1 + n]
+    x.copy_(activations(m, k, dtype, seed=off))
+    qa.qr_linear(fmt, x, w, n, gated=gated, y=y)
+    check_product(y, x, weight64(fmt, p, wide, k, dtype), n, gated, dtype, (fmt, dtype, gated, k, off))
+    rest = out.clone()
+    rest[1:-1, 1:1 + n] = 7.0
+    assert (rest == 7.0).all()
+    clean = y.clone()
+    x[1, k // 2], x[m - 1, k - 1] = float("nan"), float("inf")
+    qa.qr_linear(fmt, x, w, n, gated=gated, y=y)
+    assert torch.equal(y[2:-1], clean[2:-1]) and torch.equal(y[0], clean[0])
+    assert y[1].isnan().all() and not y[-1].isfinite().all()
+
+
 # ---------------------------------------------------------------------------
 # experts
 # ---------------------------------------------------------------------------

@@ -652,8 +652,10 @@ struct FewRows {
     }
     if constexpr (kAsym) {
       const uint32_t b = gblock + ks, tile = (b >> 6) * TB, in = (b & 63) >> 2;
-      load_value_to_lds<2>(w + (tile + Format<F>::kScaleOffset + in * 2), scales);
-      load_value_to_lds<1>(w + (tile + Format<F>::kZeroOffset + in), scales + 256);
+      if (lane < 32) {  // the other half would ask for the same again
+        load_value_to_lds<2>(w + (tile + Format<F>::kScaleOffset + in * 2), scales);
+        load_value_to_lds<1>(w + (tile + Format<F>::kZeroOffset + in), scales + 256);
+      }
     } else {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {

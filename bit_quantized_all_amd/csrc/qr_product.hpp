@@ -1,16 +1,23 @@
 // qr_product.hpp -- gfx950 kernels of the products with 4-bit block weights
 // (include/qr_ops.h): y = x W^T for one weight or one per group of rows.
 //
-// All products run on the matrix unit as v_mfma_f32_16x16x32: A is a fragment
-// of 16 weight rows, B one of 16 rows of x, each lane (r = lane & 15, g = lane
-// >> 4) holding 8 consecutive k of row r, and the result has, in that lane,
-// four consecutive weight rows 4 g .. 4 g + 3 of x row r: a lane stores
-// neighbouring values of one row of y.
+// y[m][c] = sum over k of x[m][k] W[c][k], W[c][k] = d[c][k / group] (code - z)
+// (FP4: d times the E2M1 value).  Three kernels, chosen by how often a weight is
+// used once it is there:
+//   row_kernel        1 or 2 rows of x: fp32 FMAs, bound by memory and the launch
+//   few_rows_kernel   up to a few tens of rows a weight: matrix unit on the
+//                     codes, scales applied to fp32 sums of a block; bound by
+//                     memory latency times what fits into LDS on its way
+//   many_rows_kernel  more: matrix unit on decoded weights; bound by the matrix
+//                     and the vector unit together
+// The first two use W as it stands, exact to fp32 rounding.  The third rounds W
+// to the call's dtype, as qr_decode does: the matrix unit takes 16-bit operands,
+// and a scale for the fp32 sum of each block of 32 would be four FMAs of the
+// vector unit for every product of 16 x 16 x 32, as long as that product itself.
 //
-// The order of k inside a product is free as long as both operands agree.  A
-// lane loads 16 bytes of codes, one 32-value block (so one scale a load), and
-// feeds them unit by unit: in step i of four, lane (r, g) supplies unit i of
-// block g of a 128-value chunk, k = 32 g + 8 i .. + 7, of both operands.
+// The matrix unit's product is 16 x 16 x 32: lane (r = lane & 15, g = lane >> 4)
+// holds 8 consecutive k, 8 g .. 8 g + 7, of row r of A and of B, and gets rows
+// 4 g .. 4 g + 3 of A's side in column r of B's.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -32,7 +39,7 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 
-constexpr int kChunk = 128;        // values of k that one 16-byte load per lane covers
+constexpr int kChunk = 128;        // values of k of the weights that the many-row kernel asks for at a time
 constexpr int kChunkBlocks = kChunk / kBlockValues;
 
 // Arguments of the product kernels.  Dense products have offsets == nullptr
@@ -335,8 +342,11 @@ __device__ __forceinline__ float wave_sum(float v) {
 // slices of 2048 values, one 32-value block a lane, so that a row's codes and
 // scales are read in whole lines.  x goes through LDS once for the workgroup
 // and stays in fp32 registers for the wave's weight rows; every product and
-// sum is an fp32 FMA.  Bound by reading the weights, and in small calls by the
-// one trip to memory: all of a slice's loads are in flight at once.
+// sum is an fp32 FMA, so W is not rounded.  Bound by reading the weights, and in
+// small calls by the launch and the one trip to memory: all of a slice's loads
+// are in flight at once.  One row, int4, 4096 x 4096 (9.4 MB): 4.6 us on the
+// device, 2.1 TB/s, where an empty kernel takes 2.5; two experts' gated 2048 x
+// 4096 (18.9 MB): 8.2 us, 2.3 TB/s.
 constexpr int kRowWaves = 8;
 constexpr int kRowsPerWave = 4;
 constexpr int kSlice = kWave * kBlockValues;
@@ -586,10 +596,11 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 // 64-byte piece it touches, 16 when four neighbouring lanes share one and 64
 // when each lane reads a row of its own, as the fragments of the matrix unit
 // want it.  So nothing is loaded in fragment order: codes, scales and x go to
-// LDS in whole runs of a row, the next segment's while one is multiplied.  There, 16-byte piece p of
-// row r (a block of codes, a unit of x) lies at place p ^ (r & 7), so that lanes
-// which read one piece of eight rows hit eight different groups of banks; the
-// lanes that load it take their pieces in that order.
+// LDS in whole runs of a row, the next segment's while one is multiplied.
+// There, 16-byte piece p of row r (a block of codes, a unit of x) lies at place
+// p ^ (r & 7), so that lanes which read one piece of eight rows hit eight
+// different groups of banks; the lanes that load it take their pieces in that
+// order.
 //
 // x is the matrix unit's A here and the weight its B, so that a lane's results
 // belong to one weight row, whose scales it applies to them: lane (r, g) has
@@ -601,6 +612,12 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 // subtraction, and sum_k x comes from one more product.  An infinity in x
 // would make that inf - inf; a wave whose sum is not finite computes it again
 // with the values c - z themselves.
+//
+// Bound by the latency of memory: a CU holds two segments of at most 16 waves,
+// 72 to 144 KB of LDS, of which half is on its way.  16 rows, asym4, gated, n =
+// k = 8192 (71 MB): 20.5 us, 3.4 TB/s; 64 tokens, 8 of 64 experts, gated, n
+// 1024, k 2048 (143 MB): 49.5 us, 2.9 TB/s; 37 rows that begin on odd
+// addresses, fp4, 5003 x 4129 (11.7 MB): 12.6 us, 0.9 TB/s.
 constexpr int kSegment = 256;
 constexpr int kSegBlocks = kSegment / kBlockValues;
 constexpr int kSegUnits = kSegment / 8;
@@ -891,10 +908,12 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 
 // A workgroup of WM x WN waves computes a tile of WM MFR 16 rows of x by WN NFR
 // 16 weight rows, each wave MFR x NFR fragments of it, in stages of 64 values
-// of k.  A stage's x and a chunk's codes and scales go to LDS without a stop in
-// registers, while the one before is multiplied.  Each wave decodes the weights it multiplies, rounded to
-// the dtype as qr_decode does, straight into the matrix unit's A: they pass LDS
-// once, in 4 bits, and the work of a decode is shared by MFR products.
+// of k.  A stage's x and a chunk's codes and scales (128 values: a load costs
+// the address unit as much for 32 bytes of a row as for 64) go to LDS without a
+// stop in registers, while the one before is multiplied.  Each wave decodes the
+// weights it multiplies, rounded to the dtype as qr_decode does, straight into
+// the matrix unit's A: they pass LDS once, in 4 bits, and the work of a decode
+// is shared by MFR products.
 //
 // LDS: row m of x is 8 units of 16 bytes, unit u at place u ^ (m & 7), so that
 // 8 lanes that read one unit of 8 rows hit 8 groups of banks; the lanes that
@@ -904,6 +923,19 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 // come in pairs whose rows interleave by fours, so that it has 8 neighbours:
 // one 16-byte store.  Gated: the first half of a wave's fragments are gate
 // rows, the second the same columns' up rows.
+//
+// Bound by the issue of matrix and vector instructions together: 3.7 of the
+// latter a product at MFR = 8, and the matrix unit busy 52 % of the time at the
+// 2.0 GHz that the full chip holds (8192 tokens, 2 of 16 experts, gated, n = k =
+// 4096, int4 bf16: 1150 us, 960 TFLOP/s; without the decode and without the
+// loads 740).  1024 x 8192 x 8192 int4 bf16: 137 us, 1000 TFLOP/s.  1000
+// tokens, 4 of 40 experts, 1001 x 2080, fp4 fp16: 49 us, where a tile's 33
+// stages are too few to hide the trips to memory that begin it.
+//
+// Slower here: products of 32 x 32 x 16 (1357 us where this kernel was at 1250,
+// with half the LDS reads but longer waits for a result), tiles of 256 x 256 for
+// 8 waves (1209 and 1110), weights of 64 values at a time (1260 and 1160), two
+// stages of x ahead with tiles of 64 x 128 (55 us and 49: fewer workgroups a CU).
 constexpr int kStage = 64;
 constexpr int kStageBlocks = kStage / kBlockValues;
 

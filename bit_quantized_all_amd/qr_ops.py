@@ -69,12 +69,12 @@ def qr_encode_weight(fmt, w, packed=None, stream=None):
     group = WEIGHT_FORMATS[fid]
     kp = -(-k // group) * group
     n = -(-rows * kp // 2048) * 2048
-    if n != rows * k:
-        with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(w.device):
+    with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(w.device):
+        if n != rows * k:
             flat = torch.zeros(n, dtype=w.dtype, device=w.device)
             flat[:rows * kp].view(rows, kp)[:, :k] = w
-    else:
-        flat = w.contiguous().view(-1)
+        else:
+            flat = w.contiguous().view(-1)
     if packed is None:
         packed = _empty(w, (nbytes,), torch.uint8, stream)
     qr_encode(fid, flat, packed, stream)

@@ -9,9 +9,12 @@
  * qr_encode packs it.  So the packed form of a [rows, k] matrix whose k is a
  * multiple of the block and whose size is a multiple of 2048 is exactly
  * qr_encode's of its rows * k values.  Padding values are zero.
- * The weight that a product uses is what qr_decode returns for the call's
- * dtype, W = dtype(code value * scale); products are summed in fp32 and the
- * result is rounded once.
+ * The weight that a product uses is W = code value * scale.  Where many rows
+ * of x share it, it is rounded to the call's dtype, which is what qr_decode
+ * returns; where few do, it is used as it is, so that y then has less error.
+ * Products are summed in fp32 and y is rounded once.  Which of the two a call
+ * takes depends on its sizes and on the alignment and stride of x only, so
+ * equal calls have equal results.
  *
  * Conventions beyond those of qr.h:
  *   - x and y are row-major with a row stride (ldx, ldy) counted in values and

@@ -199,9 +199,9 @@ struct CombineArgs {
 
 // A thread sums 8 neighbouring columns of one token, in the order of the
 // slots, in fp32.  Bound by reading the expert rows and writing the sums: 32768
-// tokens with 2 rows each, a twentieth dropped, n 4096 fp16 (780 MB): 144 us, 5.4
-// TB/s.  64 tokens with 8 rows, n 2048: 4.8 us on the device, where an empty
-// kernel takes 2.5.
+// tokens with 2 rows each, a twentieth dropped, n 4096 fp16 (780 MB): 139 us, 5.6
+// TB/s (144 with every load by the way of a row's end).  64 tokens with 8 rows, n
+// 2048: 4.3 us on the device, where an empty kernel takes 2.5.
 template <int DT>
 __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs a) {
   const int cols = 1 << a.lane_bits;
@@ -216,7 +216,8 @@ __global__ __launch_bounds__(kCombineThreads) void combine_kernel(CombineArgs a)
     const int p = pos[j];
     if (p < 0 || p >= a.slots) continue;
     const float w = gates[j];
-    const u32x4 v = load_x8_tail(a.y + 2 * p * a.ldy, c, a.n);
+    const uint8_t* row = a.y + 2 * p * a.ldy;
+    const u32x4 v = c + 8 <= a.n ? *reinterpret_cast<const u32x4_any*>(row + 2 * (size_t)c) : load_x8_tail(row, c, a.n);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       s[2 * i] = __builtin_fmaf(w, lo_to_f32<DT>(v[i]), s[2 * i]);

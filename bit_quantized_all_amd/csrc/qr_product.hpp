@@ -475,28 +475,28 @@ __global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
 // 16 bytes from each lane's address to lds + 16 lane, which is the same for the
 // whole wave.  In assembly, because the compiler would wait for it before the
 // next LDS read of any address, also of the buffer that is not being written;
-// it has no result that a register waits for.  M0 holds the LDS address; nothing
-// else here uses it.  Who reads the bytes waits with loads_done() and a barrier.
+// it has no result that a register waits for.  M0 holds the LDS address.  Who
+// reads the bytes waits with loads_done() and a barrier.
 __device__ __forceinline__ uint32_t lds_address(void* lds) {
   return (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
 }
 __device__ __forceinline__ void load_to_lds(const uint8_t* p, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
 }
 // One value of SIZE bytes (1 or 2, zero-extended) from each lane's address to lds + 4 lane.
 template <int SIZE>
 __device__ __forceinline__ void load_value_to_lds(const uint8_t* p, uint32_t lds) {
   if constexpr (SIZE == 2)
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
   else
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" : : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(p) : "memory", "m0");
 }
 // The same from a base of the whole wave plus each lane's offset.
 __device__ __forceinline__ void load_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
                :
                : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
-               : "memory");
+               : "memory", "m0");
 }
 template <int SIZE>
 __device__ __forceinline__ void load_value_to_lds(const uint8_t* base, uint32_t offset, uint32_t lds) {
@@ -504,12 +504,12 @@ __device__ __forceinline__ void load_value_to_lds(const uint8_t* base, uint32_t 
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ushort %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
   else
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2"
                  :
                  : "s"(__builtin_amdgcn_readfirstlane(lds)), "v"(offset), "s"(base)
-                 : "memory");
+                 : "memory", "m0");
 }
 // A barrier of the workgroup that leaves loads to LDS on their way, which
 // __syncthreads() would wait for; each wave's LDS accesses are done before it.

@@ -8,12 +8,13 @@
 //   few_rows_kernel   up to a few tens of rows a weight: matrix unit on the
 //                     codes, scales applied to fp32 sums of a block; bound by
 //                     memory latency times what fits into LDS on its way
-//   many_rows_kernel  more: matrix unit on decoded weights; bound by the matrix
-//                     and the vector unit together
-// The first two use W as it stands, exact to fp32 rounding.  The third rounds W
-// to the call's dtype, as qr_decode does: the matrix unit takes 16-bit operands,
-// and a scale for the fp32 sum of each block of 32 would be four FMAs of the
-// vector unit for every product of 16 x 16 x 32, as long as that product itself.
+//   many_rows_kernel  more: the same in large tiles; bound by the issue of
+//                     instructions, mostly the vector unit's
+// All of them use W as it stands, and only y is rounded to the dtype.  The matrix
+// unit takes 16-bit operands, which hold a code (less its zero point) exactly
+// but not its product with an fp16 scale; so the scale is applied to the fp32 sum
+// of a block.  That is four FMAs of the vector unit for every product of 16 x 16
+// x 32, which take as long to issue as the product takes the matrix unit.
 //
 // The matrix unit's product is 16 x 16 x 32: lane (r = lane & 15, g = lane >> 4)
 // holds 8 consecutive k, 8 g .. 8 g + 7, of row r of A and of B, and gets rows
@@ -162,93 +163,6 @@ __device__ __forceinline__ RawBlock load_raw(const uint8_t* w, uint32_t b) {
     r.zero = 0;
   }
   return r;
-}
-
-// What decode_unit() needs of a block's scale.  The decoded weight is
-// dtype(value * d), the rounding of qr_decode.  For fp16, value is an exact
-// fp16 and one packed multiply rounds the product; for bf16 the product is
-// exact in fp32 and the conversion to bf16 rounds it.
-template <int F, int DT>
-struct BlockScale;
-template <int F>
-struct BlockScale<F, kFp16> {
-  f16x2 d, off;  // off: what takes 1024 + code to the signed value
-  __device__ __forceinline__ BlockScale() {}
-  __device__ __forceinline__ explicit BlockScale(const RawBlock& r) {
-    const _Float16 s = __builtin_bit_cast(_Float16, (uint16_t)r.scale);
-    d = f16x2{s, s};
-    if constexpr (Format<F>::kAsym) {
-      // fp16 patterns of 1024 + z, negated
-      const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(0xE400u + r.zero));
-      off = f16x2{z, z};
-    } else {
-      off = f16x2{(_Float16)-1032.0f, (_Float16)-1032.0f};
-    }
-  }
-};
-template <int F>
-struct BlockScale<F, kBf16> {
-  float d, off;  // value * d = (code / 512) * (512 d) + off, both products exact
-  __device__ __forceinline__ BlockScale() {}
-  __device__ __forceinline__ explicit BlockScale(const RawBlock& r) {
-    const float s = (float)__builtin_bit_cast(_Float16, (uint16_t)r.scale);
-    if constexpr (Format<F>::kFp4) {
-      d = s;
-      off = 0.0f;
-    } else if constexpr (Format<F>::kAsym) {
-      d = s * 512.0f;
-      off = (float)r.zero * -s;
-    } else {
-      d = s * 512.0f;
-      off = s * -8.0f;
-    }
-  }
-};
-
-// The 8 values of one unit word as four packed pairs of the dtype.
-template <int F, int DT>
-__device__ __forceinline__ u32x4 decode_unit(uint32_t w, const BlockScale<F, DT>& s) {
-  u32x4 o;
-  if constexpr (Format<F>::kFp4) {
-    if constexpr (DT == kFp16) {
-      // the conversions' scale operand is a power of two: 1, and the block
-      // scale is multiplied in afterwards
-      o.x = __builtin_bit_cast(uint32_t, (f16x2)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0) * s.d));
-      o.y = __builtin_bit_cast(uint32_t, (f16x2)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1) * s.d));
-      o.z = __builtin_bit_cast(uint32_t, (f16x2)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2) * s.d));
-      o.w = __builtin_bit_cast(uint32_t, (f16x2)(__builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3) * s.d));
-    } else {
-      const f32x2 a = fp4_unpack<0>(w), b = fp4_unpack<1>(w), c = fp4_unpack<2>(w), d = fp4_unpack<3>(w);
-      o.x = pack2<kBf16>(a.x * s.d, a.y * s.d);
-      o.y = pack2<kBf16>(b.x * s.d, b.y * s.d);
-      o.z = pack2<kBf16>(c.x * s.d, c.y * s.d);
-      o.w = pack2<kBf16>(d.x * s.d, d.y * s.d);
-    }
-  } else {
-    const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
-    if constexpr (DT == kFp16) {
-      const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
-      // bytes c 0x64: the fp16 value 1024 + c
-      auto pair = [&](uint32_t v, uint32_t sel) {
-        const uint32_t t = __builtin_amdgcn_perm(0x64646464u, v, sel);
-        return __builtin_bit_cast(uint32_t, (f16x2)((__builtin_bit_cast(f16x2, t) + s.off) * s.d));
-      };
-      o.x = pair(a, 0x04010400u);
-      o.y = pair(a, 0x04030402u);
-      o.z = pair(b, 0x04010400u);
-      o.w = pair(b, 0x04030402u);
-    } else {
-      // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
-      const f32x2 v02 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, false), v46 = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo, true);
-      const f32x2 v13 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, false), v57 = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi, true);
-      auto val = [&](float c) { return __builtin_fmaf(c, s.d, s.off); };
-      o.x = pack2<kBf16>(val(v02.x), val(v13.x));
-      o.y = pack2<kBf16>(val(v02.y), val(v13.y));
-      o.z = pack2<kBf16>(val(v46.x), val(v57.x));
-      o.w = pack2<kBf16>(val(v46.y), val(v57.y));
-    }
-  }
-  return o;
 }
 
 // ---------------------------------------------------------------------------
@@ -906,36 +820,83 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 // many rows
 // ---------------------------------------------------------------------------
 
+// The 8 values of a unit without the scale, a pair at a time: exact in either
+// dtype.  In bf16, which has the range of fp32, they are 1 / kStep of what they
+// stand for, so that no sum over a block of 32 is larger than the largest |x|.
+template <int F, int DT>
+struct UnitPairs {
+  static constexpr float kStep = DT == kFp16 ? 1.0f : Format<F>::kFp4 ? 256.0f : 512.0f;
+  uint32_t a, b;
+  __device__ __forceinline__ void set(uint32_t w) {
+    if constexpr (Format<F>::kFp4) {
+      a = w;
+    } else {
+      const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
+      a = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
+      b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+    }
+  }
+  template <int J>
+  __device__ __forceinline__ uint32_t pair(uint32_t zero) const {
+    if constexpr (Format<F>::kFp4) {
+      if constexpr (DT == kFp16)
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, J));
+      else
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, 1.0f / kStep, J));
+    } else if constexpr (DT == kFp16) {
+      // bytes c 0x64 are the fp16 value 1024 + c; 0xE400 + zero is -1024 - zero
+      const uint32_t t = __builtin_amdgcn_perm(0x64646464u, J & 2 ? b : a, J & 1 ? 0x04030402u : 0x04010400u);
+      const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(0xE400u + (Format<F>::kAsym ? zero : 8u)));
+      return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, t) + f16x2{z, z}));
+    } else {
+      // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
+      const float z = (float)zero * (1.0f / kStep);
+      const f32x2 v = __builtin_amdgcn_cvt_pk_f32_fp8((int)(J & 2 ? b : a), (J & 1) != 0);
+      return pack2<DT>(v.x - z, v.y - z);
+    }
+  }
+};
+
 // A workgroup of WM x WN waves computes a tile of WM MFR 16 rows of x by WN NFR
 // 16 weight rows, each wave MFR x NFR fragments of it, in stages of 64 values
 // of k.  A stage's x and a chunk's codes and scales (128 values: a load costs
 // the address unit as much for 32 bytes of a row as for 64) go to LDS without a
 // stop in registers, while the one before is multiplied.  Each wave decodes the
-// weights it multiplies, rounded to the dtype as qr_decode does, straight into
-// the matrix unit's A: they pass LDS once, in 4 bits, and the work of a decode
-// is shared by MFR products.
+// weights it multiplies, codes less zero points, straight into the matrix unit's
+// B: they pass LDS once, in 4 bits, and the work of a decode is shared by MFR
+// products.  x is the unit's A, so that a lane's results belong to one weight
+// row, whose scale it applies to them.
 //
 // LDS: row m of x is 8 units of 16 bytes, unit u at place u ^ (m & 7), so that
 // 8 lanes that read one unit of 8 rows hit 8 groups of banks; the lanes that
 // load it take their units in that order.
 //
-// A lane's results are 4 neighbouring weight rows of one row of x.  Fragments
-// come in pairs whose rows interleave by fours, so that it has 8 neighbours:
-// one 16-byte store.  Gated: the first half of a wave's fragments are gate
-// rows, the second the same columns' up rows.
+// A lane's results are 4 rows of x in one column.  The column fragments of a
+// wave interleave (lane r of fragment f has column OUT r + f), so that a lane
+// has OUT neighbours of a row and 16 lanes a run of it.  Gated: the first half of
+// a wave's fragments are gate rows, the second the same columns' up rows.
 //
-// Bound by the issue of matrix and vector instructions together: 3.7 of the
-// latter a product at MFR = 8, and the matrix unit busy 52 % of the time at the
-// 2.0 GHz that the full chip holds (8192 tokens, 2 of 16 experts, gated, n = k =
-// 4096, int4 bf16: 1150 us, 960 TFLOP/s; without the decode and without the
-// loads 740).  1024 x 8192 x 8192 int4 bf16: 137 us, 1000 TFLOP/s.  1000
-// tokens, 4 of 40 experts, 1001 x 2080, fp4 fp16: 49 us, where a tile's 33
-// stages are too few to hide the trips to memory that begin it.
+// A wave goes through the weight fragments of a step of 32 values of k one
+// after another, each by all rows of x: x stays in registers for the step, and
+// only two decoded fragments do, the present and the next.
 //
-// Slower here: products of 32 x 32 x 16 (1357 us where this kernel was at 1250,
-// with half the LDS reads but longer waits for a result), tiles of 256 x 256 for
-// 8 waves (1209 and 1110), weights of 64 values at a time (1260 and 1160), two
-// stages of x ahead with tiles of 64 x 128 (55 us and 49: fewer workgroups a CU).
+// Bound by the issue of instructions: a product takes 4 FMAs for the scale and
+// (int4 bf16, MFR = 8) 2.6 for its share of a decode, 8.3 in all, of 4 cycles
+// each, where it keeps the matrix unit busy for 16.  8192 tokens, 2 of 16 experts,
+// gated, n = k = 4096, int4 bf16: 1380 us, 800 TFLOP/s; without the scales'
+// FMAs 1114, without the decode 1164, without the loads 1230, without the last
+// two 974.  1024 x 8192 x 8192 int4 bf16: 167 us, 820 TFLOP/s.  1000 tokens, 4 of
+// 40 experts, 1001 x 2080, fp4 fp16: 51 us, where a tile's 33 stages are too few
+// to hide the trips to memory that begin it.  Weights rounded to the dtype
+// before the product need no FMAs for the scale: 1160, 137 and 49 us, with errors
+// of 2.9e-3, 2.4e-3 and 2.7e-4 instead of the 1.7e-3, 1.7e-3 and 2.1e-4 that the
+// rounding of y has.
+//
+// Slower here: a wave that goes through all fragments row by row of x (1480 us:
+// four decoded fragments and their successors leave registers for two rows of x),
+// branches around loads past the end (1450 us), tiles of 256 x 128 (1950) and 128
+// x 256 (1920) for 8 waves in grouped products, tiles of 128 x 128 (1360 at best,
+// but 186 instead of 167 for 2048 rows, gated, of 4096 x 4096 fp16).
 constexpr int kStage = 64;
 constexpr int kStageBlocks = kStage / kBlockValues;
 
@@ -960,8 +921,7 @@ template <int F, int DT, bool GATED, int WM, int WN, int MFR, int NFR, bool ALIG
 __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs a) {
   constexpr int WAVES = WM * WN, HALVES = GATED ? 2 : 1;
   constexpr int OUT = NFR / HALVES;               // column fragments of y of one wave
-  constexpr int PAIR = OUT > 1 ? 2 : 1;
-  static_assert(OUT * HALVES == NFR && OUT % PAIR == 0, "whole pairs of fragments, or one");
+  static_assert(OUT * HALVES == NFR, "as many gate as up fragments");
   constexpr int BM = 16 * WM * MFR, BN = 16 * WN * NFR;
   constexpr int COLS = 16 * NFR / HALVES;         // columns of y of one wave
   constexpr int XI = BM / 8 / WAVES;              // loads of x of one wave in a stage: 8 rows each
@@ -969,7 +929,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
   constexpr int WL = BN / 16 / WAVES;             // loads of codes of one wave in a chunk: a fragment's rows each
   static_assert(WL * 16 * WAVES == BN && WL <= MFR, "the waves share the loads of codes evenly");
   static_assert(XI <= MFR, "a load of x goes with each row of the first step's products");
-  static_assert(MFR % NFR == 0, "one fragment is decoded every MFR / NFR rows of products");
+  constexpr int kAhead = MFR >= 8 ? 1 : 2;        // fragments between the read of codes and their decode
   constexpr uint32_t TB = Format<F>::kTileBytes;
   constexpr bool kAsym = Format<F>::kAsym;
   struct Weights {
@@ -977,9 +937,9 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     uint32_t scales[BN][kChunkBlocks];              // asymmetric: the group's, four times
     uint32_t zeros[kAsym ? BN : 1][kChunkBlocks];
   };
-  // The first step of a chunk is decoded while the last of the one before it is
-  // multiplied: a chunk is asked for in the first stage of the one before it,
-  // and in LDS by its second.
+  // The first fragment of a stage is decoded while the last of the one before it
+  // is multiplied, and x of its first step read: a stage's x is asked for a stage
+  // ahead, and a chunk's weights in the second stage of the one before it.
   __shared__ u32x4 lds_x[2][BM][8];
   __shared__ Weights lds_w[2];
 
@@ -1009,7 +969,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     for (int l = 0; l < WL; ++l) {
       const int part = WAVES * l + wave, f = part % NFR, q = lane >> 2;
       const int half = f / OUT, ff = f % OUT;
-      const int in = COLS * (part / NFR) + (PAIR == 2 ? 32 * (ff >> 1) + 8 * (q >> 2) + 4 * (ff & 1) + (q & 3) : q);
+      const int in = COLS * (part / NFR) + OUT * q + ff;
       const long long first = (row0 + (long long)half * a.n) * a.blocks;
       wbase[l] = a.w + (first >> 6) * TB;
       wblock[l] = (uint32_t)(first & 63) + (uint32_t)(n0 + in < a.n ? in : a.n - 1 - n0) * (uint32_t)a.blocks;
@@ -1037,19 +997,13 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
         load_value_to_lds<1>(wbase[l], at + Format<F>::kZeroOffset + (in >> 2),
                              to + (uint32_t)(offsetof(Weights, zeros) + 256 * part));
     };
-    // Rows that begin on 16 bytes (ALIGNED) go to LDS directly, and where a row
-    // ends, zeros instead; others pass through registers.
+    // Rows that begin on 16 bytes (ALIGNED) go to LDS directly, others pass through
+    // registers.  Stages past the last repeat the row's end, for nobody.
     auto fetch_x = [&](int st, int buf, int i) {
       if constexpr (ALIGNED) {
         const uint32_t to = lds_address(&lds_x[0][0][0]) + (uint32_t)(BM * 128 * buf + 1024 * (XI * wave + i));
-        const uint8_t* from = a.x + 2 * kStage * (size_t)st;
-        if (kStage * (st + 1) <= a.k) {
-          load_to_lds(from, xoff[i], to);
-        } else if (kStage * st + 8 * unit < a.k) {
-          load_to_lds(from, xoff[i], to);
-        } else {
-          lds_x[buf][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = u32x4{0u, 0u, 0u, 0u};
-        }
+        const uint32_t in = (uint32_t)(kStage * st + 8 * unit), end = (uint32_t)a.k - 8;
+        load_to_lds(a.x, xoff[i] + 2 * (in < end ? in : end), to);
       } else {
         if (kStage * (st + 1) <= a.k)
           xv[i] = *reinterpret_cast<const u32x4_any*>(xrow[i] + 2 * kStage * (size_t)st);
@@ -1057,23 +1011,42 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
           xv[i] = load_x8_tail(xrow[i] - 16 * unit, kStage * st + 8 * unit, a.k);
       }
     };
-    u32x4 wv[NFR];
-    uint32_t code[NFR], scale[NFR], zero[NFR];
-    // codes and scales of block b of a chunk
-    auto read_step = [&](const Weights& w, int b) {
-#pragma unroll
-      for (int f = 0; f < NFR; ++f) {
-        const int R = 16 * (NFR * wn + f) + r, p = b ^ (r >> 2);
-        code[f] = reinterpret_cast<const uint32_t*>(&w.codes[R][p])[g];
-        scale[f] = w.scales[R][p];
-        zero[f] = kAsym ? w.zeros[kAsym ? R : 0][p] : 0u;
-      }
+    // A step is 32 values of k, one block: fragment s = NFR b + f of a stage is
+    // weight fragment f in step b.  While the products of one fragment are
+    // issued, the next one is decoded and the codes of the kAhead-th next are
+    // read from LDS.
+    constexpr int kSteps = kStageBlocks * NFR;
+    const int p0 = r >> 2;
+    u32x4 wv[2], x[MFR];
+    float d[2];
+    uint32_t code[kAhead], scale[kAhead], zero[kAhead];
+    auto read_codes = [&](const Weights& w, int block, int f, int slot) {
+      const int R = 16 * (NFR * wn + f) + r, p = block ^ p0;
+      code[slot] = reinterpret_cast<const uint32_t*>(&w.codes[R][p])[g];
+      scale[slot] = w.scales[R][p];
+      zero[slot] = kAsym ? w.zeros[kAsym ? R : 0][p] : 8u;
     };
-    auto decode = [&](int f) {
-      RawBlock raw;
-      raw.scale = scale[f];
-      raw.zero = zero[f];
-      return decode_unit<F, DT>(code[f], BlockScale<F, DT>(raw));
+    UnitPairs<F, DT> unit_of;
+    auto decode = [&](u32x4& to, int slot, int j) {
+      if (j == 0) unit_of.set(code[slot]);
+      if (j == 0) to.x = unit_of.template pair<0>(zero[slot]);
+      if (j == 1) to.y = unit_of.template pair<1>(zero[slot]);
+      if (j == 2) to.z = unit_of.template pair<2>(zero[slot]);
+      if (j == 3) to.w = unit_of.template pair<3>(zero[slot]);
+    };
+    auto scale_of = [&](int slot) {
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)scale[slot]) * UnitPairs<F, DT>::kStep;
+    };
+    // The block's scale is applied to a product's sums kLag products later, when they are there.
+    constexpr int kLag = 3, kRing = 4;
+    static_assert(MFR % kRing == 0 && NFR % 2 == 0, "rings begin anew with each fragment, and with each step");
+    f32x4 part[kRing];
+    auto add_part = [&](int q) {  // product q of a step, from -kLag on
+      const int f = q < 0 ? NFR - 1 : q / MFR, i = (q + MFR) % MFR;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+        acc[i][f][t] = __builtin_fmaf(d[f & 1], part[(q + kRing) % kRing][t], acc[i][f][t]);
+      asm volatile("" : "+v"(acc[i][f]));  // here, not where the loop ends
     };
 
     // The first weights need not wait for the numbers of the rows of x, which are
@@ -1084,108 +1057,129 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
     for (int i = 0; i < XI; ++i) {
       const int m = rt.m0 + 8 * (XI * wave + i) + (lane >> 3);
       const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
-      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx + 16 * unit;
+      const long long at = 2 * (s < 0 ? 0 : s) * a.ldx;
       if constexpr (ALIGNED)
         xoff[i] = (uint32_t)at;
       else
-        xrow[i] = a.x + at;
+        xrow[i] = a.x + at + 16 * unit;
     }
 #pragma unroll
     for (int i = 0; i < XI; ++i) fetch_x(0, 0, i);
-    for (int st = 0; st < stages; ++st) {
-      const int h = st & 1, wb = (st >> 1) & 1;  // stage of the chunk; where its weights are
+    // Everything asked for is there, x of stage `st` in buffer `buf`, for every wave, and every
+    // wave has read what lay in the buffers that are asked for next.
+    auto arrived = [&](int st, int buf) {
       loads_done<0>();
       if constexpr (!ALIGNED) {
 #pragma unroll
-        for (int i = 0; i < XI; ++i) lds_x[h][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
+        for (int i = 0; i < XI; ++i) lds_x[buf][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = xv[i];
+      } else if (kStage * (st + 1) > a.k) {  // zeros past the row's end
+        if (kStage * st + 8 * unit >= a.k) {
+#pragma unroll
+          for (int i = 0; i < XI; ++i)
+            lds_x[buf][8 * (XI * wave + i) + (lane >> 3)][lane & 7] = u32x4{0u, 0u, 0u, 0u};
+        }
       }
       stage_barrier();
-      if (st == 0) {
-        read_step(lds_w[0], 0);
+    };
+    arrived(0, 0);
 #pragma unroll
-        for (int f = 0; f < NFR; ++f) wv[f] = decode(f);
-      }
-      if (h == 0 && st + 2 < stages) {
+    for (int i = 0; i < XI; ++i) fetch_x(1, 1, i);
+    auto read_x = [&](int buf, int b, int i) { x[i] = lds_x[buf][16 * (MFR * wm + i) + r][(4 * b + g) ^ (r & 7)]; };
 #pragma unroll
-        for (int l = 0; l < WL; ++l) fetch_weights((st >> 1) + 1, 1 - wb, l);
-      }
-      const u32x4(*xs)[8] = &lds_x[h][16 * MFR * wm + r];
+    for (int s = 0; s < kAhead; ++s) read_codes(lds_w[0], 0, s, s);
 #pragma unroll
-      for (int b = 0; b < kStageBlocks; ++b) {
-        // This step's products, with the next step's decode and the next
-        // loads in between: the matrix unit and the vector unit work side by
-        // side.  The compiler would decode first and multiply then; it is
-        // held to this order.
-        if (b + 1 < kStageBlocks)
-          read_step(lds_w[wb], kStageBlocks * h + b + 1);
+    for (int i = 0; i < MFR; ++i) read_x(0, 0, i);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) decode(wv[0], 0, j);
+    d[0] = scale_of(0);
+    d[1] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kRing; ++q) part[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    // Stage st, the first (H = 0) or second of a chunk whose weights are in buffer wb.
+    auto multiply = [&](auto H, int st, int wb) __attribute__((always_inline)) {
+      constexpr int h = decltype(H)::value;
+#pragma unroll
+      for (int s = 0; s < kSteps; ++s) {
+        const int b = s / NFR, f = s % NFR;
+        // The next stage's x, and the next chunk's weights if it begins one, have to be
+        // there kAhead fragments before the end, and the x of this one is in registers by then.
+        if (s == kSteps - kAhead) arrived(st + 1, 1 - h);
+        const int to = s + kAhead;  // whose codes are read
+        if (to < kSteps)
+          read_codes(lds_w[wb], kStageBlocks * h + to / NFR, to % NFR, to % kAhead);
         else
-          read_step(lds_w[h ? 1 - wb : wb], kStageBlocks * (1 - h));
-        u32x4 next[NFR], x[MFR];
-#pragma unroll
-        for (int i = 0; i < 2; ++i) x[i] = xs[16 * i][(4 * b + g) ^ (r & 7)];
+          read_codes(lds_w[h ? 1 - wb : wb], kStageBlocks * (1 - h), to % NFR, to % kAhead);
         __builtin_amdgcn_sched_barrier(0);
+        // The matrix unit and the vector unit work side by side: a product, then the scaling
+        // of an earlier one's sums and a pair of the next fragment's values.  The compiler would
+        // put them one after another; it is held to this order.
 #pragma unroll
         for (int i = 0; i < MFR; ++i) {
-          constexpr int kEvery = MFR / NFR, kPer = (XI + NFR - 1) / NFR;
-          if (i + 2 < MFR) x[i + 2] = xs[16 * (i + 2)][(4 * b + g) ^ (r & 7)];
-#pragma unroll
-          for (int f = 0; f < NFR; ++f) acc[i][f] = mfma<DT>(wv[f], x[i], acc[i][f]);
-          if (i % kEvery == kEvery - 1) {
-            next[i / kEvery] = decode(i / kEvery);
-            asm volatile("" : "+v"(next[i / kEvery]));
-#pragma unroll
-            for (int j = 0; j < kEvery; ++j) {
-              __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-#pragma unroll
-              for (int f = 0; f < NFR; ++f) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x002, (24 + kEvery * NFR - 1) / (kEvery * NFR), 0);
-              }
-            }
+          part[i % kRing] = mfma<DT>(x[i], wv[s & 1], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          add_part(f * MFR + i - kLag);
+          if (i >= MFR - 4) decode(wv[(s + 1) & 1], (s + 1) % kAhead, i - (MFR - 4));
+          if (i == MFR - 1) {
+            d[(s + 1) & 1] = scale_of((s + 1) % kAhead);
+            asm volatile("" : "+v"(wv[(s + 1) & 1]), "+v"(d[(s + 1) & 1]));
+          }
+          if (f == NFR - 1) read_x(b ? 1 - h : h, 1 - b, i);
+          __builtin_amdgcn_sched_barrier(0);
+          if (s == kSteps - 1 && i < XI) {
+            fetch_x(st + 2, h, i);
             __builtin_amdgcn_sched_barrier(0);
-            if (b == 0 && st + 1 < stages) {
-#pragma unroll
-              for (int l = (i / kEvery) * kPer; l < XI && l < (i / kEvery + 1) * kPer; ++l) fetch_x(st + 1, 1 - h, l);
-              __builtin_amdgcn_sched_barrier(0);
-            }
+          }
+          if (s == 0 && i < WL && h) {
+            fetch_weights((st >> 1) + 1, 1 - wb, i);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
-#pragma unroll
-        for (int f = 0; f < NFR; ++f) wv[f] = next[f];
       }
+    };
+    for (int st = 0; st < stages; st += 2) {
+      multiply(std::integral_constant<int, 0>{}, st, (st >> 1) & 1);
+      if (st + 1 < stages) multiply(std::integral_constant<int, 1>{}, st + 1, (st >> 1) & 1);
     }
+    loads_done<0>();  // what was asked for past the end: LDS is the next workgroup's soon
+#pragma unroll
+    for (int q = -kLag; q < 0; ++q) add_part(q);
   }
 
+  // which of the wave's rows have a source: bit m & 63 of word m / 64
+  unsigned long long sources[MFR / 4];
+#pragma unroll
+  for (int q = 0; q < MFR / 4; ++q) {
+    const int m = rt.m0 + 16 * MFR * wm + 64 * q + lane;
+    sources[q] = __ballot(!rt.zero && m < rt.m1 && source_row(a, m) >= 0);
+  }
 #pragma unroll
   for (int i = 0; i < MFR; ++i) {
-    const int m = rt.m0 + 16 * (MFR * wm + i) + r;
-    if (m >= rt.m1) continue;
-    const bool real = !rt.zero && source_row(a, m) >= 0;
-    uint8_t* row = a.y + 2 * (long long)m * a.ldy;
+    const int in = 16 * (MFR * wm + i) + 4 * g, c = n0 + COLS * wn + OUT * r;
 #pragma unroll
-    for (int p = 0; p < OUT; p += PAIR) {
-      float v[4 * PAIR];
+    for (int t = 0; t < 4; ++t) {
+      if (rt.m0 + in + t >= rt.m1) continue;
+      const bool real = (sources[i / 4] >> (16 * (i % 4) + 4 * g + t)) & 1;
+      uint8_t* to = a.y + 2 * ((long long)(rt.m0 + in + t) * a.ldy + c);
+      float v[OUT + 1];
 #pragma unroll
-      for (int e = 0; e < PAIR; ++e)
+      for (int p = 0; p < OUT; ++p) {
+        const float h = acc[i][p][t];
+        v[p] = !real ? 0.0f : GATED ? gate(h, acc[i][p + (GATED ? OUT : 0)][t]) : h;
+      }
+      v[OUT] = 0.0f;
+      uint16_t o[OUT + 1];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float h = acc[i][p + e][j];
-          v[4 * e + j] = !real ? 0.0f : GATED ? gate(h, acc[i][p + e + (GATED ? OUT : 0)][j]) : h;
-        }
-      const int c = n0 + COLS * wn + 16 * p + 4 * PAIR * g;
-      uint32_t o[2 * PAIR];
-#pragma unroll
-      for (int j = 0; j < 2 * PAIR; ++j) o[j] = pack2<DT>(v[2 * j], v[2 * j + 1]);
-      if (c + 4 * PAIR <= a.n) {
-        if constexpr (PAIR == 2)
-          *reinterpret_cast<u32x4_any*>(row + 2 * (size_t)c) = u32x4{o[0], o[1], o[2], o[3]};
-        else
-          *reinterpret_cast<u32x2_any*>(row + 2 * (size_t)c) = u32x2{o[0], o[1]};
+      for (int p = 0; p < OUT; p += 2) {
+        const uint32_t two = pack2<DT>(v[p], v[p + 1]);
+        o[p] = (uint16_t)two;
+        o[p + 1] = (uint16_t)(two >> 16);
+      }
+      if (c + OUT <= a.n) {
+        __builtin_memcpy(to, o, 2 * OUT);
       } else {
 #pragma unroll
-        for (int j = 0; j < 4 * PAIR; ++j)
-          if (c + j < a.n)
-            *reinterpret_cast<uint16_t*>(row + 2 * (size_t)(c + j)) = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+        for (int p = 0; p < OUT; ++p)
+          if (c + p < a.n) reinterpret_cast<uint16_t*>(to)[p] = o[p];
       }
     }
   }

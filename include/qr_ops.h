@@ -9,12 +9,10 @@
  * qr_encode packs it.  So the packed form of a [rows, k] matrix whose k is a
  * multiple of the block and whose size is a multiple of 2048 is exactly
  * qr_encode's of its rows * k values.  Padding values are zero.
- * The weight that a product uses is W = code value * scale.  Where many rows
- * of x share it, it is rounded to the call's dtype, which is what qr_decode
- * returns; where few do, it is used as it is, so that y then has less error.
- * Products are summed in fp32 and y is rounded once.  Which of the two a call
- * takes depends on its sizes and on the alignment and stride of x only, so
- * equal calls have equal results.
+ * The weight that a product uses is W = code value * scale, which is not
+ * rounded to the call's dtype first; products are summed in fp32 and y is
+ * rounded once.  The order of the sums depends on the call's sizes and on the
+ * alignment and stride of x only, so equal calls have equal results.
  *
  * Conventions beyond those of qr.h:
  *   - x and y are row-major with a row stride (ldx, ldy) counted in values and

@@ -1,0 +1,86 @@
+"""Products whose sums are exact, so that nothing but the one rounding of the result is left to
+compare, at any depth and whichever kernel a call reaches (MI355X only).
+
+x holds -1, 0 and 1, at most 250 of them not zero in a row.  Scales are fp16 values of one
+binade [2^-6, 2^-5), all 11 bits of them in use, or zero.  Every weight, and every partial sum in whatever
+order, is then a multiple of 2^-16, and below 250 * 30 * 2^-5 < 2^8 in magnitude, the codes' and the zero points'
+sums apart too (FP4, whose values are halves: multiples of 2^-17 below 250 * 6 * 2^-5 < 2^7).  These are fewer
+than 2^24 steps, so fp32 holds all of them, and y has to be the sum rounded once to the dtype, bit for bit.  A
+product that rounds its weights first, or leaves one out, differs.
+"""
+import numpy as np
+import pytest
+import torch
+
+from product_rule import variant
+from test_ops_gpu import DT, GROUP, HALF_ULP, TINY, qa, random_packed, weight64  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = sorted(GROUP)
+
+
+def exact_packed(fmt, rows, k, seed):
+    p = random_packed(fmt, rows, k, seed)
+    groups = 2048 // GROUP[fmt]
+    rng = np.random.default_rng(seed + 1)
+    s = ((1024 + rng.integers(0, 1024, (p.shape[0], groups))) * 2.0 ** -16).astype(np.float16)
+    s[rng.random(s.shape) < 0.02] = 0
+    p[:, 1024:1024 + 2 * groups] = s.view(np.uint8).reshape(p.shape[0], -1)
+    return p
+
+
+def signs(m, k, seed):
+    rng = np.random.default_rng(seed)
+    x = np.where(rng.random((m, k)) < min(1.0, 200 / k), rng.choice([-1.0, 1.0], (m, k)), 0.0)
+    x[np.cumsum(x != 0, axis=1) > 250] = 0
+    x[:, k - 1] = np.where(np.arange(m) % 2, 1.0, -1.0)   # the last value always counts
+    return torch.from_numpy(x)
+
+
+def sums(fmt, packed, rows, k, x):
+    """x W^T in fp64 on the GPU, exact; checks that fp32 holds every partial sum."""
+    _, w, apart = weight64(fmt, packed, rows, k, "fp16")
+    w, apart, x = torch.from_numpy(w).cuda(), torch.from_numpy(apart).cuda(), x.double().cuda()
+    assert torch.mm(x.abs(), apart.t().contiguous()).max() < (2.0 ** 7 if fmt == "fp4" else 2.0 ** 8)
+    return torch.mm(x, w.t().contiguous())
+
+
+def check(y, h, n, gated, dtype, what):
+    if not gated:
+        assert torch.equal(y, h.to(DT[dtype])), what
+        return
+    g, u = h[:, :n], h[:, n:]
+    want = g / (1 + torch.exp(-g)) * u
+    tol = ((g.abs() + 8) * 2.0 ** -23 + HALF_ULP[dtype]) * want.abs() * (1 + 2.0 ** -8) + TINY[dtype]
+    assert ((y.double() - want).abs() <= tol).all(), what
+
+
+def linear(qa, fmt, dtype, gated, m, n, k, off=0):
+    """One product against its exact sums; ``off``: x begins that many values into rows of k + off."""
+    wide = n * (2 if gated else 1)
+    p = exact_packed(fmt, wide, k, m + n + k)
+    x = signs(m, k, m * k + n)
+    big = torch.zeros(m, k + off, dtype=DT[dtype], device="cuda")
+    big[:, off:] = x.to(DT[dtype])
+    y = qa.qr_linear(fmt, big[:, off:], torch.from_numpy(p.reshape(-1)).cuda(), n, gated=gated)
+    check(y, sums(fmt, p, wide, k, x), n, gated, dtype, (fmt, dtype, gated, m, n, k, off))
+
+
+MANY = [("many", 64, 128, True), ("many", 64, 128, False), ("many", 256, 128, True), ("many", 128, 256, True)]
+MANY_SHAPES = [(700, 3300, 200), (130, 16500, 64), (2100, 1100, 8200), (700, 3300, 203), (2100, 1100, 8205),
+               (1300, 4500, 72), (1024, 8192, 456), (2050, 4500, 328), (2305, 8200, 136)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("dtype", sorted(DT))
+@pytest.mark.parametrize("gated", [False, True])
+def test_many_rows_use_the_weight_as_it_is(qa, fmt, dtype, gated):
+    """The weight is not rounded to the dtype before it is multiplied, in any of the tiles."""
+    reached = set()
+    for m, n, k in MANY_SHAPES:
+        n = (n + 1) // 2 if gated else n
+        print(f"exact {fmt} {dtype} gated={gated} {m}x{n}x{k}", flush=True)
+        reached.add(variant(m, n, k, gated, fmt))
+        linear(qa, fmt, dtype, gated, m, n, k)
+    assert reached == set(MANY)

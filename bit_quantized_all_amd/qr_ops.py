@@ -7,6 +7,7 @@ fallback path.
 """
 import ctypes
 import functools
+import math
 
 import torch
 
@@ -63,13 +64,14 @@ def qr_encode_weight(fmt, w, packed=None, stream=None):
         raise ValueError(f"format {fmt!r} holds no weights (one of int4, asym4, fp4)")
     if w.dim() < 2:
         raise ValueError("w must have rows of k values")
-    w = w.reshape(-1, w.shape[-1])
-    rows, k = w.shape
+    rows, k = math.prod(w.shape[:-1]), w.shape[-1]
     nbytes = _weight_bytes(fid, rows, k)
     group = WEIGHT_FORMATS[fid]
     kp = -(-k // group) * group
     n = -(-rows * kp // 2048) * 2048
+    # every copy, that of a weight whose dimensions do not merge too, is made on the call's stream
     with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(w.device):
+        w = w.reshape(rows, k)
         if n != rows * k:
             flat = torch.zeros(n, dtype=w.dtype, device=w.device)
             flat[:rows * kp].view(rows, kp)[:, :k] = w

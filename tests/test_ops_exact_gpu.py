@@ -84,3 +84,18 @@ def test_many_rows_use_the_weight_as_it_is(qa, fmt, dtype, gated):
         reached.add(variant(m, n, k, gated, fmt))
         linear(qa, fmt, dtype, gated, m, n, k)
     assert reached == set(MANY)
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("shape", [(6, 512, 256), (5, 96, 70)])
+def test_weight_packed_on_another_stream(qa, fmt, shape):
+    """A weight that has to be copied, packed on a stream that the weight's own does not wait for."""
+    w = torch.randn(*shape, generator=torch.Generator().manual_seed(1)).half().cuda()
+    for view in (w.transpose(1, 2), w[:, 8:72], w.flip(0).transpose(0, 1)):
+        want = qa.qr_encode_weight(fmt, view)
+        torch.cuda.synchronize()
+        s = torch.cuda.Stream()
+        got = qa.qr_encode_weight(fmt, view, stream=s)
+        other = torch.zeros(view.numel(), dtype=w.dtype, device="cuda")   # memory that a copy may have been freed to
+        s.synchronize()
+        assert torch.equal(got, want) and not other.any()

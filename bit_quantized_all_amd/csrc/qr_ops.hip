@@ -33,7 +33,12 @@ static qr_status launch_1d(void (*kernel)(P...), long long groups, int threads, 
 
 constexpr int kRouteThreads = 1024;
 constexpr int kRouteWaves = kRouteThreads / kWave;
-constexpr int kRouteChunk = 2048;      // slots of one workgroup of a large plan
+// A large plan: 2048 slots a workgroup, up to 512 workgroups (two a CU, as many as
+// run at a time), and in larger plans equal parts.  Each of them adds up the
+// counts of all, so that their number has to be bounded for the work to grow
+// as the slots do: 8.4 million slots of 256 experts 111 us, 134 million 1.40 ms.
+constexpr int kRouteChunk = 2048;
+constexpr int kRouteChunks = 512;
 constexpr int kRouteSmall = 4096;      // slots up to which one workgroup does it all
 static_assert(QR_MAX_EXPERTS <= kRouteThreads, "one thread per expert");
 
@@ -306,8 +311,17 @@ static qr_status product(qr_format fmt, qr_dtype dtype, int gated, const void* x
   }
 }
 
+// Slots of one workgroup: whole steps of its threads.
+static size_t route_per_chunk(size_t slots) {
+  if (slots <= (size_t)kRouteSmall) return slots;
+  if (slots <= (size_t)kRouteChunk * kRouteChunks) return kRouteChunk;
+  const size_t part = (slots + kRouteChunks - 1) / kRouteChunks;
+  return (part + kRouteThreads - 1) / kRouteThreads * kRouteThreads;
+}
+
 static int route_chunks(size_t slots) {
-  return slots <= (size_t)kRouteSmall ? 1 : (int)((slots + kRouteChunk - 1) / kRouteChunk);
+  const size_t per = route_per_chunk(slots);
+  return slots <= per ? 1 : (int)((slots + per - 1) / per);
 }
 
 static bool bad_plan(size_t tokens, size_t top, size_t experts) {
@@ -368,7 +382,7 @@ qr_status qr_route(const void* ids, int id_bytes, int32_t* offsets, int32_t* row
   a.top = (int)top;
   a.experts = (int)experts;
   a.chunks = route_chunks(slots);
-  a.per_chunk = a.chunks == 1 ? a.slots : kRouteChunk;
+  a.per_chunk = (int)route_per_chunk(slots);
   hipStream_t st = (hipStream_t)stream;
   if (a.chunks > 1) {
     const qr_status s = launch_1d(id_bytes == 4 ? route_count_kernel<int32_t> : route_count_kernel<int64_t>, a.chunks,

@@ -76,7 +76,9 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // Row tile `t` of the launch: experts in order, each cut into tiles of BM
 // rows, and then the rows of no expert.  One wave finds it (every wave on its
 // own, no exchange): a lane takes an expert, counts its tiles, and a scan over
-// the lanes shows which expert's range holds t.  64 experts a step.
+// the lanes shows which expert's range holds t.  64 experts a step.  An offset
+// below an earlier one counts as that one, so that no two groups share a row
+// and the launch has a tile for every row.
 template <int BM>
 __device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t) {
   RowTile rt;
@@ -89,13 +91,24 @@ __device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t) {
   }
   const int lane = threadIdx.x & (kWave - 1);
   int before = 0;  // tiles of the experts of earlier steps
+  int top = 0;     // where the last of them ends
   for (int e0 = 0; e0 <= a.experts; e0 += kWave) {
     const int e = e0 + lane;  // e == experts: the rows of no expert
-    int lo = 0, hi = 0;
+    int lo = a.slots, hi = a.slots;
     if (e <= a.experts) {
       lo = clampi(a.offsets[e], 0, a.slots);
       hi = e < a.experts ? clampi(a.offsets[e + 1], 0, a.slots) : a.slots;
     }
+    if (__any(lo < top || hi < lo)) {  // out of order: each becomes the largest up to it
+      lo = lo > top ? lo : top;
+#pragma unroll
+      for (int s = 1; s < kWave; s <<= 1) {
+        const int o = __shfl_up(lo, s);
+        if (lane >= s && o > lo) lo = o;
+      }
+      hi = hi > lo ? hi : lo;
+    }
+    top = __builtin_amdgcn_readlane(hi, kWave - 1);
     const int mine = hi > lo ? (hi - lo + BM - 1) / BM : 0;
     int upto = mine;
 #pragma unroll
@@ -121,9 +134,9 @@ __device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t) {
   return rt;
 }
 
-// Largest number of row tiles that find_rows() can hand out: no more groups
-// than rows are not empty, each has a tile that holds at least one row, and the
-// other tiles are full.
+// Largest number of row tiles that find_rows() can hand out: the groups share no
+// row, no more of them than there are rows are not empty, each of these has a tile
+// that holds at least one row, and the other tiles are full.
 inline long long row_tiles(long long slots, long long experts, bool dense, int bm) {
   if (dense) return (slots + bm - 1) / bm;
   const long long groups = experts + 1 < slots ? experts + 1 : slots;

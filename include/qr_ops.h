@@ -65,9 +65,9 @@ qr_status qr_linear(qr_format fmt, qr_dtype dtype, int gated, const void *x, siz
  *   offsets  device, experts + 1 int32, ascending from 0: rows offsets[e] to
  *            offsets[e + 1] of y belong to expert e.  The rows from
  *            offsets[experts] on belong to none and are set to zero.
- *            (Offsets are clamped to [0, slots]; a group whose end lies before
- *            its beginning is empty; a row that no group covers is left as it
- *            is, and one that two groups cover holds the result of either.)
+ *            (Offsets out of range or order: each is clamped to [0, slots], and
+ *            one below an earlier one counts as that one, which leaves its
+ *            expert's group empty.  Rows before offsets[0] are left as they are.)
  *   rows     device, `slots` int32: row s of y is computed from row rows[s] of
  *            x (a number outside [0, tokens): the row is set to zero); NULL: from
  *            row s, and tokens must be at least slots (QR_ERR_SIZE)

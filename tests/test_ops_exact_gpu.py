@@ -99,3 +99,29 @@ def test_weight_packed_on_another_stream(qa, fmt, shape):
         other = torch.zeros(view.numel(), dtype=w.dtype, device="cuda")   # memory that a copy may have been freed to
         s.synchronize()
         assert torch.equal(got, want) and not other.any()
+
+
+ORDERS = [[0, 1000, 0, 1600], [0, 1500, 0, 1500], [0, 0, 1600, 3], [7, 3, 900, 100], [1600, 0, 5, 0], [-4, 2000, 10, 1600]]
+
+
+@pytest.mark.parametrize("fmt,dtype,gated", [("int4", "fp16", False), ("asym4", "bf16", True)])
+@pytest.mark.parametrize("scale,n,kind", [(200, 40, "row"), (16, 40, "few"), (1, 40, "few"), (1, 4200, "many")])
+def test_offsets_out_of_order(qa, fmt, dtype, gated, scale, n, kind):
+    """Offsets count as the largest up to them: every row from the first on is written, by one group."""
+    k, slots = 64, 1600 // scale
+    wide = n * (2 if gated else 1)
+    rng = np.random.default_rng(n)
+    orders = [([v // scale for v in o], 3) for o in ORDERS]
+    orders += [(rng.integers(-slots // 4, slots * 5 // 4, 71 if scale == 1 else 68).tolist(), 70 if scale == 1 else 67)]
+    for o, experts in orders:
+        if experts == 3:
+            assert variant(slots, n, k, gated, fmt, experts=3)[0] == kind
+        w = torch.from_numpy(exact_packed(fmt, experts * wide, k, 3).reshape(-1)).cuda()
+        x = signs(slots, k, 5).to(DT[dtype]).cuda()
+        y = torch.full((2, slots + 2, n), float("nan"), dtype=DT[dtype], device="cuda")
+        for i, offsets in enumerate((o, np.maximum.accumulate(np.clip(o, 0, slots)))):
+            qa.qr_experts(fmt, x, w, n, torch.tensor(np.array(offsets), dtype=torch.int32).cuda(), gated=gated, y=y[i, 1:-1])
+        first = min(max(o[0], 0), slots)
+        print(f"offsets {o[:8]} of {slots} rows, {kind}", flush=True)
+        assert torch.equal(y[0, 1 + first:-1], y[1, 1 + first:-1]) and not y[0, 1 + first:-1].isnan().any()
+        assert y[0, :1 + first].isnan().all() and y[0, -1].isnan().all()

@@ -90,8 +90,9 @@ def build_test_helpers(quiet=True):
     """Test-only HIP libraries: a helper that exercises the codec's device
     functions directly, and the library itself built with its grid capped at 3
     workgroups, so that every kernel's grid-stride loop (and the encode's
-    prefetch of the next tile) runs at small sizes."""
-    build(out=SMALL_GRID_LIB, extra=["-DQR_MAX_GROUPS=3"], quiet=quiet)
+    prefetch of the next tile) runs at small sizes; the layer operators' calls
+    are made of launches of at most 2^15 threads there."""
+    build(out=SMALL_GRID_LIB, extra=["-DQR_MAX_GROUPS=3", "-DQR_MAX_LAUNCH_THREADS=32768"], quiet=quiet)
     build_abi_check()
     return build(out=TEST_HELPER_LIB, sources=TEST_HELPER_SRCS, quiet=quiet)
 

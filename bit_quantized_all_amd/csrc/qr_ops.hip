@@ -10,10 +10,9 @@
 
 namespace qr {
 
+// (The caller sees to it that a launch holds fewer than 2^32 threads.)
 template <typename... P>
 static qr_status launch_1d(void (*kernel)(P...), long long groups, int threads, hipStream_t st, P... args) {
-  // a launch holds fewer than 2^32 threads
-  if (groups * threads > 0xffffffffLL) return QR_ERR_SIZE;
   void* argv[] = {static_cast<void*>(&args)...};
   return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)groups), dim3(threads), argv, 0, st) ==
                  hipSuccess
@@ -421,9 +420,21 @@ qr_status qr_combine(qr_dtype dtype, const void* y, size_t ldy, size_t slots, co
   while ((1 << a.lane_bits) < cols && (1 << a.lane_bits) < kCombineThreads) ++a.lane_bits;
   a.col_groups = (cols + (1 << a.lane_bits) - 1) >> a.lane_bits;
   const int per_group = kCombineThreads >> a.lane_bits;
-  const long long groups = (((long long)tokens + per_group - 1) / per_group) * a.col_groups;
-  return launch_1d(dtype == QR_FP16 ? combine_kernel<kFp16> : combine_kernel<kBf16>, groups, kCombineThreads,
-                   (hipStream_t)stream, a);
+  // as many tokens at a time as a launch holds (the columns of one group of them always fit)
+  static_assert((QR_MAX_N / 8 + kCombineThreads) * 1LL < 0xffffffffLL, "a group of tokens fits a launch");
+  const long long fit = kMaxLaunchThreads / ((long long)a.col_groups * kCombineThreads);
+  const long long most = (fit > 1 ? fit : 1) * per_group;
+  for (long long t = 0; t < (long long)tokens; t += most) {
+    const long long now = (long long)tokens - t < most ? (long long)tokens - t : most;
+    a.tokens = (int)now;
+    a.pos = pos + t * a.top;
+    a.gates = gates + t * a.top;
+    a.out = (uint8_t*)out + 2 * t * a.ldo;
+    const qr_status s = launch_1d(dtype == QR_FP16 ? combine_kernel<kFp16> : combine_kernel<kBf16>,
+                                  (now + per_group - 1) / per_group * a.col_groups, kCombineThreads, (hipStream_t)stream, a);
+    if (s != QR_OK) return s;
+  }
+  return QR_OK;
 }
 
 }  // extern "C"

@@ -1,19 +1,27 @@
 // qr_product.hip -- instantiations and launches of the product kernels for one
 // weight format (QR_PRODUCT_FMT: 4 = INT4, 20 = ASYM4, 36 = FP4).
+#include "qr_ops.h"
 #include "qr_product.hpp"
 
 namespace qr {
 
-// Launches `kernel` for row tiles of `bm` rows and column tiles of `bc` columns of y.
+// Launches `kernel` for row tiles of `bm` rows and column tiles of `bc` columns
+// of y, as many row tiles at a time as a launch holds (one always fits: at most
+// n / 4 column tiles of 512 threads).
 static qr_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs a, int bm, int bc, int threads, hipStream_t st) {
+  static_assert(QR_MAX_N / 4 * 512LL < 0xffffffffLL, "a row tile fits a launch");
   a.ntiles = (a.n + bc - 1) / bc;
-  const long long groups = row_tiles(a.slots, a.experts, !a.offsets, bm) * a.ntiles;
-  if (groups * threads > 0xffffffffLL) return QR_ERR_SIZE;  // a launch holds fewer than 2^32 threads
-  void* argv[] = {&a};
-  return hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)groups), dim3(threads), argv, 0, st) ==
-                 hipSuccess
-             ? QR_OK
-             : QR_ERR_HIP;
+  const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, bm);
+  const long long fit = kMaxLaunchThreads / ((long long)a.ntiles * threads), most = fit > 1 ? fit : 1;
+  for (long long t = 0; t < tiles; t += most) {
+    const long long now = tiles - t < most ? tiles - t : most;
+    a.tile0 = (int)t;
+    void* argv[] = {&a};
+    if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)(now * a.ntiles)), dim3(threads), argv, 0,
+                        st) != hipSuccess)
+      return QR_ERR_HIP;
+  }
+  return QR_OK;
 }
 
 template <int F, int DT, bool GATED, int MR, int KS>

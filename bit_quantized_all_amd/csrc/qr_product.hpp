@@ -40,6 +40,13 @@ typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;
 typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 
+// A launch holds fewer than 2^32 threads; a call of more is made of several
+// launches.  (A small limit lets small calls run that way too.)
+#ifndef QR_MAX_LAUNCH_THREADS
+#define QR_MAX_LAUNCH_THREADS 0xffffffff
+#endif
+constexpr long long kMaxLaunchThreads = QR_MAX_LAUNCH_THREADS;
+
 constexpr int kChunk = 128;        // values of k of the weights that the many-row kernel asks for at a time
 constexpr int kChunkBlocks = kChunk / kBlockValues;
 
@@ -59,6 +66,7 @@ struct ProductArgs {
   int k;
   int blocks;           // 32-value blocks of one (padded) weight row
   int ntiles;           // column tiles of the grid
+  int tile0;            // row tile that the launch begins with
 };
 
 // ---------------------------------------------------------------------------
@@ -288,7 +296,7 @@ __global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int ks = wave % KS, c0 = (blockIdx.x % a.ntiles) * COLS;
-  RowTile rt = find_rows<MR>(a, blockIdx.x / a.ntiles);
+  RowTile rt = find_rows<MR>(a, a.tile0 + blockIdx.x / a.ntiles);
   if (rt.m0 >= rt.m1) return;
   rt.zero |= a.xrows == 0;  // every row number is out of range then
   long long src[MR];
@@ -747,7 +755,7 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
   const int kw = wave / NW, nw = wave % NW;
   const int r = lane & 15, g = lane >> 4;
   const int nt = blockIdx.x % a.ntiles;
-  RowTile rt = find_rows<16 * MF>(a, blockIdx.x / a.ntiles);
+  RowTile rt = find_rows<16 * MF>(a, a.tile0 + blockIdx.x / a.ntiles);
   if (rt.m0 >= rt.m1) return;
   rt.zero |= a.xrows == 0;  // every row number is out of range then
   const int n0 = nt * 16 * NF;
@@ -961,7 +969,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
   const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
   const TileIndex ti = tile_index(blockIdx.x, gridDim.x, a.ntiles);
-  RowTile rt = find_rows<BM>(a, ti.row);
+  RowTile rt = find_rows<BM>(a, a.tile0 + ti.row);
   if (rt.m0 >= rt.m1) return;
   rt.zero |= a.xrows == 0;  // every row number is out of range then
   const int n0 = ti.col * (BN / HALVES);

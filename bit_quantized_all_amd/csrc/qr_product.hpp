@@ -223,6 +223,13 @@ __device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 c) {
                                                    0);
 }
 
+// bf16 has the range of fp32, so a sum of codes times x could overflow where the
+// scaled sum does not (x of the type's lowest value).  There the products take
+// 1 / kStep of the values: no sum over a block of 32 is then larger than the
+// largest |x|, and kStep, a power of two, goes into the scale.
+template <int F, int DT>
+constexpr float kStep = DT == kFp16 ? 1.0f : Format<F>::kFp4 ? 256.0f : 512.0f;
+
 // silu(g) * u in fp32.
 __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + __expf(-g)) * u; }
 
@@ -230,19 +237,24 @@ __device__ __forceinline__ float gate(float g, float u) { return g / (1.0f + __e
 // one or two rows
 // ---------------------------------------------------------------------------
 
-// The 8 values of a unit in fp32, without the scale.
-template <int F>
+// The 8 values of a unit in fp32, without the scale and in steps of 1 / kStep;
+// INT4: 16 times the values.  `zero` is in the same steps.
+template <int F, int DT>
 __device__ __forceinline__ void unit_f32(uint32_t w, float zero, float (&v)[8]) {
+  constexpr float step = 1.0f / kStep<F, DT>;
   if constexpr (Format<F>::kFp4) {
-    const f32x2 a = fp4_unpack<0>(w), b = fp4_unpack<1>(w), c = fp4_unpack<2>(w), d = fp4_unpack<3>(w);
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, step, 0);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, step, 1);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, step, 2);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, step, 3);
     v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y; v[4] = c.x; v[5] = c.y; v[6] = d.x; v[7] = d.y;
   } else if constexpr (Format<F>::kAsym) {
     // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
     const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
-    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.0f, false);
-    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.0f, true);
-    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.0f, false);
-    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.0f, true);
+    const f32x2 a = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.0f * step, false);
+    const f32x2 b = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(lo, 512.0f * step, true);
+    const f32x2 c = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.0f * step, false);
+    const f32x2 d = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(hi, 512.0f * step, true);
     v[0] = a.x - zero; v[2] = a.y - zero; v[4] = b.x - zero; v[6] = b.y - zero;
     v[1] = c.x - zero; v[3] = c.y - zero; v[5] = d.x - zero; v[7] = d.y - zero;
   } else {
@@ -347,6 +359,9 @@ __global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
       if (q < XC) lds_x[q ^ ((q >> 4) & 3)] = xv[t];
     }
     __syncthreads();
+    // INT4's bytes become fp32 as they are, so there x takes the step, and the bytes' 16
+    constexpr bool kStepX = !Format<F>::kAsym && !Format<F>::kFp4 && DT == kBf16;
+    constexpr float kX = kStepX ? 1.0f / (16.0f * kStep<F, DT>) : 1.0f;
     float x[MR][kBlockValues];
 #pragma unroll
     for (int m = 0; m < MR; ++m)
@@ -356,8 +371,8 @@ __global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
         const u32x4 v = lds_x[q ^ ((q >> 4) & 3)];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          x[m][8 * u + 2 * i] = lo_to_f32<DT>(v[i]);
-          x[m][8 * u + 2 * i + 1] = hi_to_f32<DT>(v[i]);
+          x[m][8 * u + 2 * i] = lo_to_f32<DT>(v[i]) * kX;
+          x[m][8 * u + 2 * i + 1] = hi_to_f32<DT>(v[i]) * kX;
         }
       }
 #pragma unroll
@@ -368,14 +383,14 @@ __global__ __launch_bounds__(kWave* kRowWaves) void row_kernel(ProductArgs a) {
 #pragma unroll
       for (int u = 0; u < 4; ++u) {
         float v[8];
-        unit_f32<F>(raw[i].codes[u], (float)raw[i].zero, v);
+        unit_f32<F, DT>(raw[i].codes[u], (float)raw[i].zero * (1.0f / kStep<F, DT>), v);
 #pragma unroll
         for (int m = 0; m < MR; ++m)
 #pragma unroll
           for (int j = 0; j < 8; ++j) t[m][j & 1] = __builtin_fmaf(v[j], x[m][8 * u + j], t[m][j & 1]);
       }
-      float d = (float)__builtin_bit_cast(_Float16, (uint16_t)raw[i].scale);
-      if constexpr (!Format<F>::kAsym && !Format<F>::kFp4) d *= 0.0625f;
+      float d = (float)__builtin_bit_cast(_Float16, (uint16_t)raw[i].scale) * kStep<F, DT>;
+      if constexpr (!Format<F>::kAsym && !Format<F>::kFp4 && !kStepX) d *= 0.0625f;
 #pragma unroll
       for (int m = 0; m < MR; ++m) acc[m][i] = __builtin_fmaf(d, t[m][0] + t[m][1], acc[m][i]);
     }
@@ -476,10 +491,11 @@ __device__ __forceinline__ u32x4 exchange_units(u32x4 c) {
   return u32x4{p[0], p[1], q[0], q[1]};
 }
 
-// The 8 values of a unit without the scale: E2M1 values; else the codes less
-// `zero` (SIGNED) or the codes themselves.
+// The 8 values of a unit without the scale, in steps of 1 / kStep: E2M1 values;
+// else the codes less `zero` (SIGNED; in the same steps) or the codes themselves.
 template <int F, int DT, bool SIGNED>
 __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
+  constexpr float step = 1.0f / kStep<F, DT>;
   u32x4 o;
   if constexpr (Format<F>::kFp4) {
     if constexpr (DT == kFp16) {
@@ -488,34 +504,34 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
       o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2));
       o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3));
     } else {
-      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 0));
-      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 1));
-      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 2));
-      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, 1.0f, 3));
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, step, 0));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, step, 1));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, step, 2));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, step, 3));
     }
   } else {
     const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
     const uint32_t a = __builtin_amdgcn_perm(hi, lo, 0x05010400u), b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
     // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
     if constexpr (SIGNED) {
-      const f32x2 v01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.0f, false);
-      const f32x2 v23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.0f, true);
-      const f32x2 v45 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.0f, false);
-      const f32x2 v67 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.0f, true);
+      const f32x2 v01 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.0f * step, false);
+      const f32x2 v23 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(a, 512.0f * step, true);
+      const f32x2 v45 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.0f * step, false);
+      const f32x2 v67 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp8(b, 512.0f * step, true);
       o.x = pack2<DT>(v01.x - zero, v01.y - zero);
       o.y = pack2<DT>(v23.x - zero, v23.y - zero);
       o.z = pack2<DT>(v45.x - zero, v45.y - zero);
       o.w = pack2<DT>(v67.x - zero, v67.y - zero);
     } else if constexpr (DT == kFp16) {
-      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f, false));
-      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f, true));
-      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f, false));
-      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f, true));
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f * step, false));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(a, 512.0f * step, true));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f * step, false));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(b, 512.0f * step, true));
     } else {
-      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, false));
-      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f, true));
-      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, false));
-      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f, true));
+      o.x = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f * step, false));
+      o.y = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(a, 512.0f * step, true));
+      o.z = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f * step, false));
+      o.w = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, 512.0f * step, true));
     }
   }
   return o;
@@ -545,8 +561,9 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 //
 // sum_k x (c - z) is taken as sum_k x c - z sum_k x: the codes need no
 // subtraction, and sum_k x comes from one more product.  An infinity in x
-// would make that inf - inf; a wave whose sum is not finite computes it again
-// with the values c - z themselves.
+// would make that inf - inf, and x of the largest values may overflow before the
+// difference; a wave whose sum is not finite computes it again with the values
+// c - z themselves.
 //
 // Bound by the latency of memory: a CU holds two segments of at most 16 waves,
 // 72 to 144 KB of LDS, of which half is on its way.  16 rows, asym4, gated, n =
@@ -666,9 +683,9 @@ struct FewRows {
     const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int m = 0; m < MF; ++m) acc[m] = none;
-    // the factor of sum_k x: the zero point where it is the same for all
-    const uint32_t factor = kAsym ? (DT == kFp16 ? 0x3C003C00u : 0x3F803F80u)   // 1
-                                  : (DT == kFp16 ? 0xC800C800u : 0xC100C100u);  // -8
+    // the factor of sum_k x: the zero point where it is the same for all; in steps
+    const uint32_t factor = kAsym ? (DT == kFp16 ? 0x3C003C00u : 0x3B003B00u)   // 1, 1 / 512
+                                  : (DT == kFp16 ? 0xC800C800u : 0xBC80BC80u);  // -8, -8 / 512
     const u32x4 factors = {factor, factor, factor, factor};
     const int segments = (a.k + kSegment - 1) / kSegment;  // each has values of x
     // every wave goes through as many rounds as the first group
@@ -710,12 +727,12 @@ struct FewRows {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // the asymmetric format's groups: blocks 4 h .. 4 h + 3
         f32x4 part[MF], sx[MF];
-        const float z = kAsym ? (float)zero[h] : 8.0f;
+        const float z = kAsym ? (float)zero[h] : 8.0f, step = 1.0f / kStep<F, DT>;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           const int b = 4 * h + q, i = b >> 1, j = b & 1;
-          const u32x4 wv = unit_values<F, DT, SIGNED>(codes[j][i], z);
-          const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)scale[kAsym ? h : b]);
+          const u32x4 wv = unit_values<F, DT, SIGNED>(codes[j][i], z * step);
+          const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)scale[kAsym ? h : b]) * kStep<F, DT>;
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
             const u32x4 x = now.x[kw][16 * m + r][(4 * b + g) ^ (r & 7)];
@@ -732,7 +749,7 @@ struct FewRows {
           }
         }
         if constexpr (kAsym && !SIGNED) {
-          const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)scale[h]);
+          const float d = (float)__builtin_bit_cast(_Float16, (uint16_t)scale[h]) * kStep<F, DT>;
 #pragma unroll
           for (int m = 0; m < MF; ++m)
 #pragma unroll
@@ -842,11 +859,10 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 // ---------------------------------------------------------------------------
 
 // The 8 values of a unit without the scale, a pair at a time: exact in either
-// dtype.  In bf16, which has the range of fp32, they are 1 / kStep of what they
-// stand for, so that no sum over a block of 32 is larger than the largest |x|.
+// dtype, and in steps of 1 / kStep.
 template <int F, int DT>
 struct UnitPairs {
-  static constexpr float kStep = DT == kFp16 ? 1.0f : Format<F>::kFp4 ? 256.0f : 512.0f;
+  static constexpr float kValue = 1.0f / kStep<F, DT>;
   uint32_t a, b;
   __device__ __forceinline__ void set(uint32_t w) {
     if constexpr (Format<F>::kFp4) {
@@ -863,7 +879,7 @@ struct UnitPairs {
       if constexpr (DT == kFp16)
         return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, J));
       else
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, 1.0f / kStep, J));
+        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, kValue, J));
     } else if constexpr (DT == kFp16) {
       // bytes c 0x64 are the fp16 value 1024 + c; 0xE400 + zero is -1024 - zero
       const uint32_t t = __builtin_amdgcn_perm(0x64646464u, J & 2 ? b : a, J & 1 ? 0x04030402u : 0x04010400u);
@@ -871,7 +887,7 @@ struct UnitPairs {
       return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, t) + f16x2{z, z}));
     } else {
       // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
-      const float z = (float)zero * (1.0f / kStep);
+      const float z = (float)zero * kValue;
       const f32x2 v = __builtin_amdgcn_cvt_pk_f32_fp8((int)(J & 2 ? b : a), (J & 1) != 0);
       return pack2<DT>(v.x - z, v.y - z);
     }
@@ -1056,7 +1072,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       if (j == 3) to.w = unit_of.template pair<3>(zero[slot]);
     };
     auto scale_of = [&](int slot) {
-      return (float)__builtin_bit_cast(_Float16, (uint16_t)scale[slot]) * UnitPairs<F, DT>::kStep;
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)scale[slot]) * kStep<F, DT>;
     };
     // The block's scale is applied to a product's sums kLag products later, when they are there.
     constexpr int kLag = 3, kRing = 4;

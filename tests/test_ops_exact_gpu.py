@@ -125,3 +125,37 @@ def test_offsets_out_of_order(qa, fmt, dtype, gated, scale, n, kind):
         print(f"offsets {o[:8]} of {slots} rows, {kind}", flush=True)
         assert torch.equal(y[0, 1 + first:-1], y[1, 1 + first:-1]) and not y[0, 1 + first:-1].isnan().any()
         assert y[0, :1 + first].isnan().all() and y[0, -1].isnan().all()
+
+
+LARGE_SHAPES = [(1, 300, 4200), (2, 300, 4200), (1, 5000, 200), (2, 400, 8229), (5, 64, 333), (12, 12300, 136), (9, 12300, 331),
+                (30, 9000, 72), (40, 64, 1032), (30, 66000, 71), (700, 3300, 200), (700, 3300, 203), (1300, 4500, 72), (2050, 4500, 72)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_values_near_the_end_of_the_range(qa, fmt):
+    """bf16 x of the type's lowest value, 255 * 2^120 in magnitude: alone among others, in a whole block and throughout
+    a row.  The sums of codes times x leave the range of fp32, the products x W and their sums do not."""
+    low = torch.finfo(torch.bfloat16).min
+    for m, n, k in LARGE_SHAPES:
+        p = exact_packed(fmt, n, k, m + n + k)
+        groups = 2048 // GROUP[fmt]
+        s = np.ascontiguousarray(p[:, 1024:1024 + 2 * groups]).view(np.float16) * np.float16(2.0 ** -6)   # [2^-12, 2^-11)
+        p[:, 1024:1024 + 2 * groups] = s.view(np.uint8).reshape(p.shape[0], -1)
+        x = torch.randn(m, k, generator=torch.Generator().manual_seed(k)).to(torch.bfloat16).cuda()
+        x[0, k // 2] = low
+        if m > 1:
+            x[m - 1, :] = low
+        if m > 2:
+            x[m // 2, :32] = -low
+            x[m // 2 + 1, k - 33:] = low
+        print(f"range {fmt} {m}x{n}x{k} {variant(m, n, k, False, fmt)}", flush=True)
+        y = qa.qr_linear(fmt, x, torch.from_numpy(p.reshape(-1)).cuda(), n).double()
+        _, w, apart = weight64(fmt, p, n, k, "bf16")
+        w, apart = torch.from_numpy(w).cuda(), torch.from_numpy(apart).cuda()
+        want = torch.mm(x.double(), w.t().contiguous())
+        err = k * 2.0 ** -23 * torch.mm(x.double().abs(), apart.t().contiguous())
+        # columns whose sum itself, or sum of magnitudes in fp32, leaves the range are not looked at
+        inside = (want.abs() + err < 2.0 ** 127) & (torch.mm(x.double().abs(), w.abs().t().contiguous()) < 2.0 ** 127)
+        tol = err + HALF_ULP["bf16"] * (want.abs() + err) + TINY["bf16"]
+        assert ((y - want).abs() <= tol)[inside].all() and inside.double().mean() >= 0.5, (fmt, m, n, k)
+        assert inside[0].all()

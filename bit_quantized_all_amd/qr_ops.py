@@ -3,7 +3,9 @@ layer whose weights are held in the 4-bit block formats.
 
 As in ``qr``: argument checks and marshalling only, the work runs in the HIP
 kernels of ``libqr.so`` on the current (or the given) stream, and there is no
-fallback path.
+fallback path.  The operators have no gradient: an input that asks for one is
+refused (ValueError) unless gradients are off (``torch.no_grad()``), so that none
+is lost in silence.  Packing takes a weight that has one, as ``detach()`` does.
 """
 import ctypes
 import functools
@@ -106,6 +108,12 @@ def _matrix(t, name, rows, cols, device, dtype):
     return t.data_ptr(), _row_stride(t, name, rows, cols)
 
 
+def _no_gradient(t, name):
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{name} asks for a gradient, which this operator does not have: "
+                         "detach it, or call under torch.no_grad()")
+
+
 def _row_stride(t, name, rows, cols):
     ld, step = t.stride()
     if step != 1 and cols > 1:
@@ -137,6 +145,7 @@ def _product_weight(fmt, experts, n, k, gated):
 def _product(fn, fmt, x, w, n, gated, y, offsets, rows, stream):
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
         raise ValueError("x must be a device matrix")
+    _no_gradient(x, "x")
     dtype = x.dtype
     dt = DTYPES.get(dtype)
     if dt is None:
@@ -234,6 +243,8 @@ def qr_combine(y, pos, gates, out=None, stream=None):
         raise ValueError("y must be a device matrix")
     if not (isinstance(pos, torch.Tensor) and pos.dim() == 2):
         raise ValueError("pos must be a device matrix")
+    _no_gradient(y, "y")
+    _no_gradient(gates, "gates")
     dtype = y.dtype
     dt = DTYPES.get(dtype)
     if dt is None:

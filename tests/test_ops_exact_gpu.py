@@ -159,3 +159,25 @@ def test_values_near_the_end_of_the_range(qa, fmt):
         tol = err + HALF_ULP["bf16"] * (want.abs() + err) + TINY["bf16"]
         assert ((y - want).abs() <= tol)[inside].all() and inside.double().mean() >= 0.5, (fmt, m, n, k)
         assert inside[0].all()
+
+
+def test_gradients_are_not_lost_in_silence(qa):
+    w = qa.qr_encode_weight("int4", torch.nn.Parameter(torch.randn(32, 64, device="cuda").half()))
+    x = torch.randn(4, 64, device="cuda").half()
+    ids = torch.zeros(4, 2, dtype=torch.int32, device="cuda")
+    offsets, rows, pos = qa.qr_route(ids, 1)
+    gates = torch.ones(4, 2, device="cuda")
+    want = qa.qr_linear("int4", x, w, 32)
+    y = qa.qr_experts("int4", x, w, 32, offsets, rows=rows)
+    out = qa.qr_combine(y, pos, gates)
+    xg, yg, gg = (t.clone().requires_grad_() for t in (x, y, gates))
+    for call in (lambda: qa.qr_linear("int4", xg, w, 32), lambda: qa.qr_linear("int4", xg * 1, w, 32, gated=False),
+                 lambda: qa.qr_experts("int4", xg, w, 32, offsets, rows=rows), lambda: qa.qr_combine(yg, pos, gates),
+                 lambda: qa.qr_combine(y, pos, gg)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad():
+            assert not call().requires_grad
+    assert torch.equal(qa.qr_linear("int4", xg.detach(), w, 32), want)
+    with torch.inference_mode():
+        assert torch.equal(qa.qr_combine(yg, pos, gg), out)

@@ -266,6 +266,18 @@ static bool overlap(const void* a, size_t na, const void* b, size_t nb) {
 // Bytes from the first to the last value of `rows` rows of `cols` 2-byte values.
 static size_t span(size_t rows, size_t ld, size_t cols) { return rows ? 2 * ((rows - 1) * ld + cols) : 0; }
 
+// Whether two matrices share a value.  Rows of one stride may lie beside each
+// other in a larger matrix (columns of it): there the distance of the first rows,
+// within a stride, tells.  A matrix of one row has the other's stride.
+static bool overlap_rows(const void* a, size_t ra, size_t lda, size_t ca, const void* b, size_t rb, size_t ldb, size_t cb) {
+  if (!overlap(a, span(ra, lda, ca), b, span(rb, ldb, cb))) return false;
+  const size_t ld = 2 * (ra > 1 ? lda : ldb);
+  if (ra > 1 && rb > 1 && lda != ldb) return true;
+  const uintptr_t a0 = (uintptr_t)a, b0 = (uintptr_t)b;
+  const size_t from = b0 >= a0 ? (b0 - a0) % ld : (ld - (a0 - b0) % ld) % ld;  // of b's row, from a's
+  return from < 2 * ca || from + 2 * cb > ld;
+}
+
 // Row strides up to 2^32 values keep every byte offset of 2^30 rows within 63 bits.
 constexpr size_t kMaxStride = (size_t)1 << 32;
 
@@ -285,7 +297,7 @@ static qr_status product(qr_format fmt, qr_dtype dtype, int gated, const void* x
   if (misaligned(x, 2) || misaligned(y, 2) || misaligned(w, 16) || misaligned(offsets, 4) || misaligned(rows, 4))
     return QR_ERR_ALIGN;
   const size_t ys = span(slots, ldy, n);
-  if (overlap(y, ys, x, span(xrows, ldx, k)) || overlap(y, ys, w, wbytes) ||
+  if (overlap_rows(y, slots, ldy, n, x, xrows, ldx, k) || overlap(y, ys, w, wbytes) ||
       (offsets && overlap(y, ys, offsets, 4 * (experts + 1))) || (rows && overlap(y, ys, rows, 4 * slots)))
     return QR_ERR_ALIAS;
   ProductArgs a = {};
@@ -402,7 +414,7 @@ qr_status qr_combine(qr_dtype dtype, const void* y, size_t ldy, size_t slots, co
   if ((!y && slots) || !pos || !gates || !out) return QR_ERR_ARG;
   if (misaligned(y, 2) || misaligned(out, 2) || misaligned(pos, 4) || misaligned(gates, 4)) return QR_ERR_ALIGN;
   const size_t os = span(tokens, ldo, n);
-  if (overlap(out, os, y, span(slots, ldy, n)) || overlap(out, os, pos, 4 * tokens * top) ||
+  if (overlap_rows(out, tokens, ldo, n, y, slots, ldy, n) || overlap(out, os, pos, 4 * tokens * top) ||
       overlap(out, os, gates, 4 * tokens * top))
     return QR_ERR_ALIAS;
   CombineArgs a = {};

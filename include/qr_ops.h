@@ -20,7 +20,9 @@
  *     aligned (QR_ERR_ALIGN).  int32 and fp32 arrays are 4-byte aligned.
  *   - Checks run on the host before any HIP call, in the order format/dtype
  *     (QR_ERR_UNSUPPORTED), sizes (QR_ERR_SIZE), null pointers (QR_ERR_ARG),
- *     alignment (QR_ERR_ALIGN), overlap of an output with anything (QR_ERR_ALIAS).
+ *     alignment (QR_ERR_ALIGN), overlap of an output with anything (QR_ERR_ALIAS;
+ *     matrices of one row stride may be columns of one larger matrix, and what
+ *     lies between the rows of other outputs counts as theirs).
  *   - A call with no rows (m, slots or tokens = 0) is complete as it is:
  *     QR_OK, and where nothing is written null pointers are accepted.
  *   - What the device arrays hold is not seen by the host: offsets that are out

@@ -181,3 +181,30 @@ def test_gradients_are_not_lost_in_silence(qa):
     assert torch.equal(qa.qr_linear("int4", xg.detach(), w, 32), want)
     with torch.inference_mode():
         assert torch.equal(qa.qr_combine(yg, pos, gg), out)
+
+
+def test_columns_of_one_matrix(qa):
+    """x and y beside each other in the rows of one buffer, either one first, and one row of y between two of x."""
+    n, k = 40, 64
+    p = exact_packed("int4", n, k, 1)
+    w = torch.from_numpy(p.reshape(-1)).cuda()
+    for m in (1, 2, 20, 700):
+        x = signs(m, k, m)
+        want = sums("int4", p, n, k, x).half()
+        for first, second in ((0, k), (n, 0), (3, k + 3)):
+            buf = torch.full((m, n + k + 3), 7.0, dtype=torch.float16, device="cuda")
+            buf[:, first:first + k] = x.half()
+            y = buf[:, second:second + n]
+            qa.qr_linear("int4", buf[:, first:first + k], w, n, y=y)
+            assert torch.equal(y, want) and torch.equal(buf[:, first:first + k], x.half().cuda())
+    x = signs(2, k, 5)
+    buf = torch.full((2, n + k), 7.0, dtype=torch.float16, device="cuda")
+    buf[:, :k] = x.half()
+    ids = torch.tensor([1], dtype=torch.int32, device="cuda")
+    qa.qr_experts("int4", buf[:, :k], w, n, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), rows=ids, y=buf[:1, k:])
+    assert torch.equal(buf[:1, k:], sums("int4", p, n, k, x)[1:].half()) and (buf[1, k:] == 7).all()
+    y = torch.randn(6, 80, device="cuda").half()
+    pos = torch.tensor([[3, 1], [0, 5], [2, 4], [-1, 0], [1, 1], [5, 5]], dtype=torch.int32, device="cuda")
+    gates = torch.rand(6, 2, device="cuda")
+    want = qa.qr_combine(y[:, :40], pos, gates)
+    assert torch.equal(qa.qr_combine(y[:, :40], pos, gates, out=y[:, 40:]), want)

@@ -38,8 +38,8 @@ static qr_status launch_rows(const ProductArgs& a, hipStream_t st) {
   // 16384 rows of 8192, 512 workgroups 17.1 us, 2048 with four waves each 21.9.
   const long long groups = row_tiles(a.slots, a.experts, !a.offsets, MR) * a.n * (GATED ? 2 : 1) /
                            (kRowWaves * kRowsPerWave);  // of KS = 1
-  if (a.blocks <= kWave || groups >= 256) return launch_row<F, DT, GATED, MR, 1>(a, st);
-  if (a.blocks <= 2 * kWave || groups >= 128) return launch_row<F, DT, GATED, MR, 2>(a, st);
+  if (a.blocks <= kWave || groups >= kCUs) return launch_row<F, DT, GATED, MR, 1>(a, st);
+  if (a.blocks <= 2 * kWave || groups >= kCUs / 2) return launch_row<F, DT, GATED, MR, 2>(a, st);
   return launch_row<F, DT, GATED, MR, 4>(a, st);
 }
 
@@ -53,7 +53,7 @@ static qr_status launch_few(const ProductArgs& a, hipStream_t st) {
 template <int F, int DT, bool GATED, bool ALIGNED>
 static qr_status launch_few_rows(int rows, const ProductArgs& a, hipStream_t st) {
   const long long quads = row_tiles(a.slots, a.experts, !a.offsets, 16) * ((a.n + 63) / 64) * (GATED ? 2 : 1);
-  if (rows > 16 && quads > 256) {
+  if (rows > 16 && quads > kCUs) {
     // two fragments of rows share a weight's decode: 64 experts with 25 rows
     // each 55 us instead of 74, 100 rows of 4096 x 4096 17 instead of 22; with
     // 8 rows an expert 52 instead of 46.  Two waves share the k axis where
@@ -66,7 +66,7 @@ static qr_status launch_few_rows(int rows, const ProductArgs& a, hipStream_t st)
   // 16384 rows of 8192, 16 rows of x: 23 us with four, 30 with twice as many
   // workgroups of half the waves; 4096 x 4096 and 8 rows 7.6 us with one
   // fragment a workgroup, 8.6 with two, 13 with four
-  if (quads >= 1024) return launch_few<F, DT, GATED, 1, 4, 1, ALIGNED>(a, st);
+  if (quads >= 4 * kCUs) return launch_few<F, DT, GATED, 1, 4, 1, ALIGNED>(a, st);
   if (quads >= 192) return launch_few<F, DT, GATED, 1, 4, 4, ALIGNED>(a, st);
   // (one wave would need over 256 registers for rows that pass through them)
   if constexpr (ALIGNED && !GATED) return launch_few<F, DT, GATED, 1, 1, 4, ALIGNED>(a, st);
@@ -95,7 +95,7 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   // tiled, 192 rows 79 and 88, 256 rows 82 and 89, 300 rows of 4096 x 4096 41 and
   // 46, 600 of 1024 x 4096 27 and 45, 40 experts with 50 rows of 1024 x 2048 41 and
   // 50; with more tiles, 320 rows of 8192 x 8192 120 and 116, 512 rows 165 and 120
-  if (rows <= 64 || tiles <= 256)
+  if (rows <= 64 || tiles <= kCUs)
     return aligned ? launch_few_rows<F, DT, GATED, true>(rows, a, st) : launch_few_rows<F, DT, GATED, false>(rows, a, st);
   if (!aligned) return launch_many<F, DT, GATED, 1, 4, 2, false>(a, st);
   // Tiles of 128 x 256 decode a weight half as often as those of 64 x 128, but
@@ -110,7 +110,7 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
     // then has two waves to alternate between.  1024 rows of 8192 x 8192 169 us
     // and 186 with 4 waves (210 with 64 x 128), 768 rows 161 and 184 (163); 1536
     // rows 320 and 294
-    if (!a.offsets && large <= 256) return launch_many<F, DT, GATED, 2, 8, 2, true>(a, st);
+    if (!a.offsets && large <= kCUs) return launch_many<F, DT, GATED, 2, 8, 2, true>(a, st);
     return launch_many<F, DT, GATED, 1, 8, 4, true>(a, st);
   }
   return launch_many<F, DT, GATED, 1, 4, 2, true>(a, st);

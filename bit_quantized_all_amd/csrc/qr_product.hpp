@@ -47,6 +47,10 @@ typedef u32x2 __attribute__((aligned(2))) u32x2_any;
 #endif
 constexpr long long kMaxLaunchThreads = QR_MAX_LAUNCH_THREADS;
 
+// The whole card.  In a partition of it the choices that count on them are less
+// apt, the results the same.
+constexpr int kCUs = 256, kXCDs = 8;
+
 constexpr int kChunk = 128;        // values of k of the weights that the many-row kernel asks for at a time
 constexpr int kChunkBlocks = kChunk / kBlockValues;
 
@@ -947,8 +951,8 @@ struct TileIndex {
   int row, col;
 };
 __device__ __forceinline__ TileIndex tile_index(int id, int total, int ncols) {
-  const int per = total / 8, rest = total % 8, xcd = id % 8;
-  const int t = xcd * per + (xcd < rest ? xcd : rest) + id / 8;
+  const int per = total / kXCDs, rest = total % kXCDs, xcd = id % kXCDs;
+  const int t = xcd * per + (xcd < rest ? xcd : rest) + id / kXCDs;
   const int rows = total / ncols, band = t / (kBand * ncols), in = t - band * kBand * ncols;
   const int height = rows - band * kBand < kBand ? rows - band * kBand : kBand;
   return {band * kBand + in % height, in / height};

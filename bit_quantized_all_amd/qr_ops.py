@@ -109,7 +109,8 @@ def _matrix(t, name, rows, cols, device, dtype):
 
 
 def _no_gradient(t, name):
-    if t.requires_grad and torch.is_grad_enabled():
+    """Of an input with ``requires_grad`` (asked by the caller: a call is microseconds)."""
+    if torch.is_grad_enabled():
         raise ValueError(f"{name} asks for a gradient, which this operator does not have: "
                          "detach it, or call under torch.no_grad()")
 
@@ -145,7 +146,8 @@ def _product_weight(fmt, experts, n, k, gated):
 def _product(fn, fmt, x, w, n, gated, y, offsets, rows, stream):
     if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
         raise ValueError("x must be a device matrix")
-    _no_gradient(x, "x")
+    if x.requires_grad:
+        _no_gradient(x, "x")
     dtype = x.dtype
     dt = DTYPES.get(dtype)
     if dt is None:
@@ -243,8 +245,10 @@ def qr_combine(y, pos, gates, out=None, stream=None):
         raise ValueError("y must be a device matrix")
     if not (isinstance(pos, torch.Tensor) and pos.dim() == 2):
         raise ValueError("pos must be a device matrix")
-    _no_gradient(y, "y")
-    _no_gradient(gates, "gates")
+    if y.requires_grad:
+        _no_gradient(y, "y")
+    if gates.requires_grad:
+        _no_gradient(gates, "gates")
     dtype = y.dtype
     dt = DTYPES.get(dtype)
     if dt is None:

@@ -230,7 +230,7 @@ __device__ __forceinline__ f32x4 mfma(u32x4 w, u32x4 x, f32x4 c) {
 // bf16 has the range of fp32, so a sum of codes times x could overflow where the
 // scaled sum does not (x of the type's lowest value).  There the products take
 // 1 / kStep of the values: no sum over a block of 32 is then larger than the
-// largest |x|, and kStep, a power of two, goes into the scale.
+// largest |x|, and kStep, a power of two, goes into the scale or into y.
 template <int F, int DT>
 constexpr float kStep = DT == kFp16 ? 1.0f : Format<F>::kFp4 ? 256.0f : 512.0f;
 
@@ -862,10 +862,10 @@ __global__ __launch_bounds__(kWave* NW* KW) void few_rows_kernel(ProductArgs a) 
 // many rows
 // ---------------------------------------------------------------------------
 
-// The 8 values of a unit without the scale, a pair at a time: exact in either
+// The 8 values of a unit without the scale, four at a time: exact in either
 // dtype, and in steps of 1 / kStep.
 template <int F, int DT>
-struct UnitPairs {
+struct UnitHalves {
   static constexpr float kValue = 1.0f / kStep<F, DT>;
   uint32_t a, b;
   __device__ __forceinline__ void set(uint32_t w) {
@@ -873,27 +873,33 @@ struct UnitPairs {
       a = w;
     } else {
       const uint32_t lo = w & 0x0F0F0F0Fu, hi = (w >> 4) & 0x0F0F0F0Fu;  // values 0 2 4 6 and 1 3 5 7
-      a = __builtin_amdgcn_perm(hi, lo, 0x05010400u);
-      b = __builtin_amdgcn_perm(hi, lo, 0x07030602u);
+      a = DT == kFp16 ? __builtin_amdgcn_perm(hi, lo, 0x05010400u) : lo;
+      b = DT == kFp16 ? __builtin_amdgcn_perm(hi, lo, 0x07030602u) : hi;
     }
   }
+  // Values 4 J .. 4 J + 3.
   template <int J>
-  __device__ __forceinline__ uint32_t pair(uint32_t zero) const {
+  __device__ __forceinline__ u32x2 four(uint32_t zero) const {
     if constexpr (Format<F>::kFp4) {
       if constexpr (DT == kFp16)
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, J));
+        return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, 2 * J)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(a, 1.0f, 2 * J + 1))};
       else
-        return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, kValue, J));
+        return u32x2{__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, kValue, 2 * J)),
+                     __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(a, kValue, 2 * J + 1))};
     } else if constexpr (DT == kFp16) {
       // bytes c 0x64 are the fp16 value 1024 + c; 0xE400 + zero is -1024 - zero
-      const uint32_t t = __builtin_amdgcn_perm(0x64646464u, J & 2 ? b : a, J & 1 ? 0x04030402u : 0x04010400u);
       const _Float16 z = __builtin_bit_cast(_Float16, (uint16_t)(0xE400u + (Format<F>::kAsym ? zero : 8u)));
-      return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, t) + f16x2{z, z}));
+      auto pair = [&](uint32_t sel) {
+        const uint32_t t = __builtin_amdgcn_perm(0x64646464u, J ? b : a, sel);
+        return __builtin_bit_cast(uint32_t, (f16x2)(__builtin_bit_cast(f16x2, t) + f16x2{z, z}));
+      };
+      return u32x2{pair(0x04010400u), pair(0x04030402u)};
     } else {
       // the byte c as FP8 E4M3 is c / 512 for every 4-bit c
       const float z = (float)zero * kValue;
-      const f32x2 v = __builtin_amdgcn_cvt_pk_f32_fp8((int)(J & 2 ? b : a), (J & 1) != 0);
-      return pack2<DT>(v.x - z, v.y - z);
+      const f32x2 v02 = __builtin_amdgcn_cvt_pk_f32_fp8((int)a, J != 0), v13 = __builtin_amdgcn_cvt_pk_f32_fp8((int)b, J != 0);
+      return u32x2{pack2<DT>(v02.x - z, v13.x - z), pack2<DT>(v02.y - z, v13.y - z)};
     }
   }
 };
@@ -922,22 +928,24 @@ struct UnitPairs {
 // only two decoded fragments do, the present and the next.
 //
 // Bound by the issue of instructions: a product takes 4 FMAs for the scale and
-// (int4 bf16, MFR = 8) 2.6 for its share of a decode, 8.3 in all, of 4 cycles
-// each, where it keeps the matrix unit busy for 16.  8192 tokens, 2 of 16 experts,
-// gated, n = k = 4096, int4 bf16: 1380 us, 800 TFLOP/s; without the scales'
-// FMAs 1114, without the decode 1164, without the loads 1230, without the last
-// two 974.  1024 x 8192 x 8192 int4 bf16: 167 us, 820 TFLOP/s.  1000 tokens, 4 of
-// 40 experts, 1001 x 2080, fp4 fp16: 51 us, where a tile's 33 stages are too few
-// to hide the trips to memory that begin it.  Weights rounded to the dtype
-// before the product need no FMAs for the scale: 1160, 137 and 49 us, with errors
-// of 2.9e-3, 2.4e-3 and 2.7e-4 instead of the 1.7e-3, 1.7e-3 and 2.1e-4 that the
-// rounding of y has.
+// (int4 bf16, MFR = 8) 2.4 instructions for its share of a decode, 8.6 with
+// itself and the rest, of 4 cycles each, where it keeps the matrix unit busy for
+// 16 (39 % of the time).  8192 tokens, 2 of 16 experts, gated, n = k = 4096, int4
+// bf16: 1366 us, 805 TFLOP/s; of 1404 on another card, 1087 without the scale's
+// FMAs, 1171 without the decode, 1236 without the loads, 975 without the last two.
+// 1024 x 8192 x 8192 int4 bf16: 165 us, 830 TFLOP/s.  1000 tokens, 4 of 40
+// experts, 1001 x 2080, fp4 fp16: 51 us, where a tile's 33 stages are too few to
+// hide the trips to memory that begin it.
 //
-// Slower here: a wave that goes through all fragments row by row of x (1480 us:
-// four decoded fragments and their successors leave registers for two rows of x),
-// branches around loads past the end (1450 us), tiles of 256 x 128 (1950) and 128
-// x 256 (1920) for 8 waves in grouped products, tiles of 128 x 128 (1360 at best,
-// but 186 instead of 167 for 2048 rows, gated, of 4096 x 4096 fp16).
+// Weights rounded to the dtype before the product need no FMAs for the scale:
+// 1164, 135 and 49 us, with errors of 2.9e-3, 2.4e-3 and 2.7e-4 instead of the
+// 1.7e-3, 1.7e-3 and 2.1e-4 that the rounding of y has.
+//
+// Slower here: branches around loads past the end (1452 us where this kernel was
+// at 1363), two products between a product and its scale instead of three (1535
+// and 1517, one 1554), tiles of 256 x 128 and of 128 x 256 for 8 waves in grouped
+// products (1950 and 1920 where it was at 1480), tiles of 128 x 128 (1523; 2048
+// rows, gated, of 4096 x 4096 int4 fp16 186 and 167).
 constexpr int kStage = 64;
 constexpr int kStageBlocks = kStage / kBlockValues;
 
@@ -1067,16 +1075,22 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       scale[slot] = w.scales[R][p];
       zero[slot] = kAsym ? w.zeros[kAsym ? R : 0][p] : 8u;
     };
-    UnitPairs<F, DT> unit_of;
+    UnitHalves<F, DT> half;
+    // Half j of a fragment's unit.
     auto decode = [&](u32x4& to, int slot, int j) {
-      if (j == 0) unit_of.set(code[slot]);
-      if (j == 0) to.x = unit_of.template pair<0>(zero[slot]);
-      if (j == 1) to.y = unit_of.template pair<1>(zero[slot]);
-      if (j == 2) to.z = unit_of.template pair<2>(zero[slot]);
-      if (j == 3) to.w = unit_of.template pair<3>(zero[slot]);
+      if (j == 0) {
+        half.set(code[slot]);
+        const u32x2 v = half.template four<0>(zero[slot]);
+        to.x = v.x;
+        to.y = v.y;
+      } else {
+        const u32x2 v = half.template four<1>(zero[slot]);
+        to.z = v.x;
+        to.w = v.y;
+      }
     };
     auto scale_of = [&](int slot) {
-      return (float)__builtin_bit_cast(_Float16, (uint16_t)scale[slot]) * kStep<F, DT>;
+      return (float)__builtin_bit_cast(_Float16, (uint16_t)scale[slot]);
     };
     // The block's scale is applied to a product's sums kLag products later, when they are there.
     constexpr int kLag = 3, kRing = 4;
@@ -1131,7 +1145,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
 #pragma unroll
     for (int i = 0; i < MFR; ++i) read_x(0, 0, i);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) decode(wv[0], 0, j);
+    for (int j = 0; j < 2; ++j) decode(wv[0], 0, j);
     d[0] = scale_of(0);
     d[1] = 0.0f;
 #pragma unroll
@@ -1153,13 +1167,13 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
           read_codes(lds_w[h ? 1 - wb : wb], kStageBlocks * (1 - h), to % NFR, to % kAhead);
         __builtin_amdgcn_sched_barrier(0);
         // The matrix unit and the vector unit work side by side: a product, then the scaling
-        // of an earlier one's sums and a pair of the next fragment's values.  The compiler would
+        // of an earlier one's sums and half of the next fragment's unit.  The compiler would
         // put them one after another; it is held to this order.
 #pragma unroll
         for (int i = 0; i < MFR; ++i) {
           part[i % kRing] = mfma<DT>(x[i], wv[s & 1], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
           add_part(f * MFR + i - kLag);
-          if (i >= MFR - 4) decode(wv[(s + 1) & 1], (s + 1) % kAhead, i - (MFR - 4));
+          if (i % 2 == MFR / 8 && i >= MFR - 4) decode(wv[(s + 1) & 1], (s + 1) % kAhead, (i - (MFR - 4)) / 2);
           if (i == MFR - 1) {
             d[(s + 1) & 1] = scale_of((s + 1) % kAhead);
             asm volatile("" : "+v"(wv[(s + 1) & 1]), "+v"(d[(s + 1) & 1]));
@@ -1204,8 +1218,8 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
       float v[OUT + 1];
 #pragma unroll
       for (int p = 0; p < OUT; ++p) {
-        const float h = acc[i][p][t];
-        v[p] = !real ? 0.0f : GATED ? gate(h, acc[i][p + (GATED ? OUT : 0)][t]) : h;
+        const float h = acc[i][p][t] * kStep<F, DT>;
+        v[p] = !real ? 0.0f : GATED ? gate(h, acc[i][p + (GATED ? OUT : 0)][t] * kStep<F, DT>) : h;
       }
       v[OUT] = 0.0f;
       uint16_t o[OUT + 1];

@@ -91,25 +91,25 @@ static qr_status launch_product(const ProductArgs& a, hipStream_t st) {
   const bool aligned = ((uintptr_t)a.x & 15) == 0 && a.ldx % 8 == 0 && a.k % 8 == 0 && a.xrows * a.ldx < (1LL << 31);
   const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, 64) * ((a.n * (GATED ? 2LL : 1LL) + 127) / 128);
   // Few rows, or no more tiles of 64 x 128 than CUs, which one workgroup of
-  // four waves would not keep busy: 64 rows of 8192 x 8192 33 us here and 88
-  // tiled, 192 rows 79 and 88, 256 rows 82 and 89, 300 rows of 4096 x 4096 41 and
-  // 46, 600 of 1024 x 4096 27 and 45, 40 experts with 50 rows of 1024 x 2048 41 and
-  // 50; with more tiles, 320 rows of 8192 x 8192 120 and 116, 512 rows 165 and 120
+  // four waves would not keep busy: 64 rows of 8192 x 8192 33 us here and 86
+  // tiled, 192 rows 82 and 84, 256 rows 82 and 84, 300 rows of 4096 x 4096 42 and
+  // 45, 600 of 1024 x 4096 27 and 44, 40 experts with 50 rows of 1024 x 2048 42 and
+  // 48; with more tiles, 320 rows of 8192 x 8192 125 and 111, 512 rows 166 and 113
   if (rows <= 64 || tiles <= kCUs)
     return aligned ? launch_few_rows<F, DT, GATED, true>(rows, a, st) : launch_few_rows<F, DT, GATED, false>(rows, a, st);
   if (!aligned) return launch_many<F, DT, GATED, 1, 4, 2, false>(a, st);
   // Tiles of 128 x 256 decode a weight half as often as those of 64 x 128, but
   // leave more of the last one of a group empty, and one of them on a CU is four
   // waves that wait alone.  Groups: 16 experts with 330 rows of 2048 x 4096 (464
-  // tiles at most) 157 us and 178, with 256 rows (384 at most, 256 that hold
-  // rows) 158 and 137, 8 with 200 rows of 4096 x 4096 (336 at most) 156 and 133, 64
-  // with 160 of 1024 x 2048 122 and 99
+  // tiles at most) 154 us and 172, with 256 rows (384 at most, 256 that hold
+  // rows) 153 and 134, 8 with 200 rows of 4096 x 4096 (336 at most) 151 and 130, 64
+  // with 160 of 1024 x 2048 120 and 94
   const long long large = row_tiles(a.slots, a.experts, !a.offsets, 128) * ((a.n * (GATED ? 2LL : 1LL) + 255) / 256);
   if (a.offsets ? large >= 420 && rows >= 192 : large >= 192) {
     // Up to one large tile a CU, 8 waves share one, of 256 x 128: each SIMD
-    // then has two waves to alternate between.  1024 rows of 8192 x 8192 169 us
-    // and 186 with 4 waves (210 with 64 x 128), 768 rows 161 and 184 (163); 1536
-    // rows 320 and 294
+    // then has two waves to alternate between.  1024 rows of 8192 x 8192 166 us
+    // and 180 with 4 waves (205 with 64 x 128), 768 rows 158 and 179 (158); 1536
+    // rows 312 and 286
     if (!a.offsets && large <= kCUs) return launch_many<F, DT, GATED, 2, 8, 2, true>(a, st);
     return launch_many<F, DT, GATED, 1, 8, 4, true>(a, st);
   }

@@ -7,7 +7,7 @@
 //   row_kernel        1 or 2 rows of x: fp32 FMAs, bound by memory and the launch
 //   few_rows_kernel   up to a few tens of rows a weight: matrix unit on the
 //                     codes, scales applied to fp32 sums of a block; bound by
-//                     memory latency times what fits into LDS on its way
+//                     vector instructions and the wait for each round of loads
 //   many_rows_kernel  more: the same in large tiles; bound by the issue of
 //                     instructions, mostly the vector unit's
 // All of them use W as it stands, and only y is rounded to the dtype.  The matrix
@@ -555,7 +555,8 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 // There, 16-byte piece p of row r (a block of codes, a unit of x) lies at place
 // p ^ (r & 7), so that lanes which read one piece of eight rows hit eight
 // different groups of banks; the lanes that load it take their pieces in that
-// order.
+// order.  Rows r and r + 8 of x meet in one group; conflicts are 0.42 to 0.54 of the
+// cycles in which LDS is active.
 //
 // x is the matrix unit's A here and the weight its B, so that a lane's results
 // belong to one weight row, whose scales it applies to them: lane (r, g) has
@@ -569,11 +570,14 @@ __device__ __forceinline__ u32x4 unit_values(uint32_t w, float zero) {
 // difference; a wave whose sum is not finite computes it again with the values
 // c - z themselves.
 //
-// Bound by the latency of memory: a CU holds two segments of at most 16 waves,
-// 72 to 144 KB of LDS, of which half is on its way.  16 rows, asym4, gated, n =
-// k = 8192 (71 MB): 20.5 us, 3.4 TB/s; 64 tokens, 8 of 64 experts, gated, n
-// 1024, k 2048 (143 MB): 49.5 us, 2.9 TB/s; 37 rows that begin on odd
-// addresses, fp4, 5003 x 4129 (11.7 MB): 12.6 us, 0.9 TB/s.
+// 16 rows, asym4, gated, n = k = 8192 (71 MB): 20.5 us, 3.4 TB/s; 64 tokens, 8
+// of 64 experts, gated, n 1024, k 2048 (143 MB): 49.3 us, 2.9 TB/s; 37 rows that
+// begin on odd addresses, fp4, 5003 x 4129 (11.7 MB): 12.7 us, 0.9 TB/s.  No one
+// part fills this time: of the cycles in which CUs are busy, the vector unit issues
+// in 43, 62 and 46 %, LDS is active in 21, 26 and 40 % (conflicts 9, 11 and 21 %),
+// the matrix unit is busy in 15, 18 and 8 %.  A CU holds two segments of at most
+// 16 waves, 72 to 144 KB of LDS, half of it on its way, and each of a workgroup's
+// rounds (8, 8 and 5) waits for all its loads.
 constexpr int kSegment = 256;
 constexpr int kSegBlocks = kSegment / kBlockValues;
 constexpr int kSegUnits = kSegment / 8;
@@ -930,7 +934,7 @@ struct UnitHalves {
 // Bound by the issue of instructions: a product takes 4 FMAs for the scale and
 // (int4 bf16, MFR = 8) 2.4 instructions for its share of a decode, 8.6 with
 // itself and the rest, of 4 cycles each, where it keeps the matrix unit busy for
-// 16 (39 % of the time).  8192 tokens, 2 of 16 experts, gated, n = k = 4096, int4
+// 16 (the vector unit issues in 87 % of the cycles, the matrix unit is busy in 40).  8192 tokens, 2 of 16 experts, gated, n = k = 4096, int4
 // bf16: 1366 us, 805 TFLOP/s; of 1404 on another card, 1087 without the scale's
 // FMAs, 1171 without the decode, 1236 without the loads, 975 without the last two.
 // 1024 x 8192 x 8192 int4 bf16: 165 us, 830 TFLOP/s.  1000 tokens, 4 of 40

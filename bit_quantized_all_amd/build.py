@@ -19,7 +19,8 @@ SOURCES = [(os.path.join(_CSRC, "qr_api.hip"), [])] + [
     (os.path.join(_CSRC, "qr_asym.hip"), [f"-DQR_ASYM_IN={f}"]) for f in (20, 24)] + [
     (os.path.join(_CSRC, "qr_fp4.hip"), [])] + [
     (os.path.join(_CSRC, "qr_ops.hip"), [])] + [
-    (os.path.join(_CSRC, "qr_product.hip"), [f"-DQR_PRODUCT_FMT={f}"]) for f in (4, 20, 36)]
+    (os.path.join(_CSRC, "qr_product.hip"), [f"-DQR_PRODUCT_FMT={f}"]) for f in (4, 20, 36)] + [
+    (os.path.join(_CSRC, "qr_rows.hip"), []), (os.path.join(_CSRC, "qr_product8.hip"), [])]
 LIB = os.path.join(HERE, "libqr.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 

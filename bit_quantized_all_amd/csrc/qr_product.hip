@@ -5,25 +5,6 @@
 
 namespace qr {
 
-// Launches `kernel` for row tiles of `bm` rows and column tiles of `bc` columns
-// of y, as many row tiles at a time as a launch holds (one always fits: at most
-// n / 4 column tiles of 512 threads).
-static qr_status launch_tiles(void (*kernel)(ProductArgs), ProductArgs a, int bm, int bc, int threads, hipStream_t st) {
-  static_assert(QR_MAX_N / 4 * 512LL < 0xffffffffLL, "a row tile fits a launch");
-  a.ntiles = (a.n + bc - 1) / bc;
-  const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, bm);
-  const long long fit = kMaxLaunchThreads / ((long long)a.ntiles * threads), most = fit > 1 ? fit : 1;
-  for (long long t = 0; t < tiles; t += most) {
-    const long long now = tiles - t < most ? tiles - t : most;
-    a.tile0 = (int)t;
-    void* argv[] = {&a};
-    if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)(now * a.ntiles)), dim3(threads), argv, 0,
-                        st) != hipSuccess)
-      return QR_ERR_HIP;
-  }
-  return QR_OK;
-}
-
 template <int F, int DT, bool GATED, int MR, int KS>
 static qr_status launch_row(const ProductArgs& a, hipStream_t st) {
   return launch_tiles(row_kernel<F, DT, GATED, MR, KS>, a, MR, kRowWaves / KS * kRowsPerWave / (GATED ? 2 : 1),

@@ -28,6 +28,7 @@
 
 #include "qr.h"
 #include "qr_codec.hpp"
+#include "qr_ops.h"
 
 namespace qr {
 
@@ -1247,6 +1248,26 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void many_rows_kernel(ProductArgs
 // ---------------------------------------------------------------------------
 // launch
 // ---------------------------------------------------------------------------
+
+// Launches `kernel` for row tiles of `bm` rows and column tiles of `bc` columns
+// of y, as many row tiles at a time as a launch holds (one always fits: at most
+// n / 4 column tiles of 512 threads).
+template <typename ARGS>
+qr_status launch_tiles(void (*kernel)(ARGS), ARGS a, int bm, int bc, int threads, hipStream_t st) {
+  static_assert(QR_MAX_N / 4 * 512LL < 0xffffffffLL, "a row tile fits a launch");
+  a.ntiles = (a.n + bc - 1) / bc;
+  const long long tiles = row_tiles(a.slots, a.experts, !a.offsets, bm);
+  const long long fit = kMaxLaunchThreads / ((long long)a.ntiles * threads), most = fit > 1 ? fit : 1;
+  for (long long t = 0; t < tiles; t += most) {
+    const long long now = tiles - t < most ? tiles - t : most;
+    a.tile0 = (int)t;
+    void* argv[] = {&a};
+    if (hipLaunchKernel(reinterpret_cast<const void*>(kernel), dim3((unsigned)(now * a.ntiles)), dim3(threads), argv, 0,
+                        st) != hipSuccess)
+      return QR_ERR_HIP;
+  }
+  return QR_OK;
+}
 
 qr_status launch_product_int4(int dt, bool gated, const ProductArgs& a, hipStream_t st);
 qr_status launch_product_asym4(int dt, bool gated, const ProductArgs& a, hipStream_t st);

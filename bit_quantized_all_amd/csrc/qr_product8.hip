@@ -8,8 +8,15 @@ static qr_status launch_fragments(const Product8Args& a, hipStream_t st) {
   return launch_tiles(fragments8_kernel<DT, GATED, MF, NF, KW>, a, 16 * MF, 16 * NF / (GATED ? 2 : 1), kWave * KW, st);
 }
 
+template <int DT, bool GATED, int WM, int WN, int MI, int NI>
+static qr_status launch_tiles8(const Product8Args& a, hipStream_t st) {
+  return launch_tiles(tiles8_kernel<DT, GATED, WM, WN, MI, NI>, a, 16 * WM * MI, 16 * WN * NI / (GATED ? 2 : 1),
+                      kWave * WM * WN, st);
+}
+
 template <int DT, bool GATED>
 static qr_status launch_dtype(const Product8Args& a, hipStream_t st) {
+  if (a.slots >= 256) return launch_tiles8<DT, GATED, 2, 4, 8, 4>(a, st);
   return launch_fragments<DT, GATED, 4, 4, 1>(a, st);
 }
 

@@ -136,6 +136,175 @@ __global__ __launch_bounds__(kWave* KW) void fragments8_kernel(Product8Args a) {
   }
 }
 
+// ---------------------------------------------------------------------------
+// tiles
+// ---------------------------------------------------------------------------
+
+// A workgroup of WM x WN waves computes a tile of 16 WM MI rows of x by 16 WN NI
+// rows of the weight, each wave MI x NI fragments.  A stage is one run of 128
+// bytes of every row; it goes to LDS without a stop in registers while the one
+// before is multiplied, in two buffers.
+//
+// LDS: a row is 8 units of 16 bytes, unit u of row R at place u ^ (R / 2 % 8), so
+// that 16 lanes that read one unit of 16 rows hit all 64 banks; the lanes that
+// load it take their units in that order.
+//
+// The column fragments of a wave interleave: row 4 q + j of fragment f is column 4
+// OUT q + 4 f + j, so that a lane has 4 OUT neighbours of a row of y and four
+// lanes a run of it.  Gated: the first half of a wave's fragments are gate rows,
+// the second the same columns' up rows.
+template <int DT, bool GATED, int WM, int WN, int MI, int NI>
+__global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a) {
+  constexpr int WAVES = WM * WN, HALVES = GATED ? 2 : 1, OUT = NI / HALVES;
+  static_assert(OUT * HALVES == NI, "as many gate as up fragments");
+  constexpr int BM = 16 * WM * MI, BN = 16 * WN * NI, COLS = 16 * OUT;  // COLS: of y of one wave
+  constexpr int XI = BM / 8 / WAVES, WI = BN / 8 / WAVES, LOADS = XI + WI;  // of one wave in a stage: 8 rows each
+  static_assert(XI * 8 * WAVES == BM && WI * 8 * WAVES == BN, "the waves share the loads evenly");
+  // A stage is 2 steps of 64 bytes, each MI slots of NI products with one fragment of x.  Fragments of x
+  // are read from LDS kAhead slots before they are multiplied, into a ring; those of the weight a step before.
+  constexpr int SLOTS = 2 * MI, kAhead = 3, kRing = 4;
+  static_assert(SLOTS % kRing == 0 && MI >= NI && MI > kAhead, "rings begin anew with each stage");
+  __shared__ i32x4 lds[2][BM + BN][8];
+
+  const int lane = threadIdx.x & (kWave - 1);
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN;
+  const int r = lane & 15, g = lane >> 4;
+  const TileIndex ti = tile_index(blockIdx.x, gridDim.x, a.ntiles);
+  RowTile rt = find_rows<BM>(a, a.tile0 + ti.row);
+  if (rt.m0 >= rt.m1) return;
+  rt.zero |= a.xrows == 0;  // every row number is out of range then
+  const int n0 = ti.col * (BN / HALVES);
+  const long long row_bytes = (long long)a.blocks * kRowRun;
+
+  i32x4 acc[MI][NI];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int f = 0; f < NI; ++f) acc[i][f] = i32x4{0, 0, 0, 0};
+
+  if (!rt.zero) {
+    auto place = [](int row) { return (row >> 1) & 7; };
+    // load l of this wave brings rows 8 (WI wave + l) + lane / 8 of the tile's weight rows; columns past the last
+    // repeat it
+    const uint8_t* wbase[WI];
+    uint32_t woff[WI];
+#pragma unroll
+    for (int l = 0; l < WI; ++l) {
+      const int R = 8 * (WI * wave + l), f = R / 16 % NI, q = R % 16 + (lane >> 3);
+      const int c = COLS * (R / 16 / NI) + 4 * OUT * (q >> 2) + 4 * (f % OUT) + (q & 3);
+      wbase[l] = a.w + (((long long)rt.expert * HALVES + f / OUT) * a.n + n0) * row_bytes;
+      woff[l] = (uint32_t)(n0 + c < a.n ? c : a.n - 1 - n0) * (uint32_t)row_bytes + 16 * ((lane & 7) ^ place(q));
+    }
+    // rows past the end repeat the last, rows of no source the first of x
+    const uint8_t* xp[XI];
+#pragma unroll
+    for (int l = 0; l < XI; ++l) {
+      const int R = 8 * (XI * wave + l) + (lane >> 3), m = rt.m0 + R;
+      const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
+      xp[l] = a.x + (s < 0 ? 0 : s) * row_bytes + 16 * ((lane & 7) ^ place(R));
+    }
+    const uint32_t base = lds_address(&lds[0][0][0]);
+    auto fetch = [&](int st, int buf, int l) {
+      const uint32_t to = base + (uint32_t)(buf * (BM + BN) * kRowRun);
+      if (l < WI)
+        load_to_lds(wbase[l < WI ? l : 0] + (size_t)st * kRowRun, woff[l < WI ? l : 0],
+                    to + (uint32_t)kRowRun * BM + 1024u * (WI * wave + l));
+      else
+        load_to_lds(xp[l < WI ? 0 : l - WI] + (size_t)st * kRowRun, to + 1024u * (XI * wave + l - WI));
+    };
+    i32x4 x[kRing], w[2][NI];
+    auto read_x = [&](int buf, int t) {
+      const int R = 16 * (MI * wm + t % MI) + r;
+      x[t % kRing] = lds[buf][R][(4 * (t / MI) + g) ^ place(r)];
+    };
+    auto read_w = [&](int buf, int s, int f) { w[s][f] = lds[buf][BM + 16 * (NI * wn + f) + r][(4 * s + g) ^ place(r)]; };
+    const int stages = a.blocks;
+#pragma unroll
+    for (int l = 0; l < LOADS; ++l) fetch(0, 0, l);
+    loads_done<0>();
+    stage_barrier();
+    if (stages > 1) {
+#pragma unroll
+      for (int l = 0; l < LOADS; ++l) fetch(1, 1, l);
+    }
+#pragma unroll
+    for (int f = 0; f < NI; ++f) read_w(0, 0, f);
+#pragma unroll
+    for (int t = 0; t < kAhead; ++t) read_x(0, t);
+    for (int st = 0; st < stages; ++st) {
+      const int buf = st & 1;
+#pragma unroll
+      for (int t = 0; t < SLOTS; ++t) {
+        const int s = t / MI, i = t % MI, left = SLOTS - t;
+        if (left == kAhead) {
+          // The next stage is there for every wave, and every wave has read the last of this one.
+          loads_done<0>();
+          __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS; a builtin, so that the compiler does not wait once more
+          asm volatile("s_barrier" ::: "memory");
+        }
+        // (after the last stage what lies there is read for nobody)
+        if (left > kAhead) read_x(buf, t + kAhead); else read_x(1 - buf, t + kAhead - SLOTS);
+        if (s == 0 && i < NI) read_w(buf, 1, i);
+        if (left <= kAhead) {
+#pragma unroll
+          for (int f = NI * (kAhead - left) / kAhead; f < NI * (kAhead - left + 1) / kAhead; ++f) read_w(1 - buf, 0, f);
+          if (st + 2 < stages) {
+#pragma unroll
+            for (int l = LOADS * (kAhead - left) / kAhead; l < LOADS * (kAhead - left + 1) / kAhead; ++l) fetch(st + 2, buf, l);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int f = 0; f < NI; ++f) acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][f], x[t % kRing], acc[i][f], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+  }
+
+  // the scales, without branches around their loads
+  const int c0 = n0 + COLS * wn + 4 * OUT * g;
+  const float* ws = a.ws + (long long)(rt.zero ? 0 : rt.expert) * HALVES * a.n;
+  float wscale[HALVES][4 * OUT], xscale[MI];
+  bool real[MI];
+#pragma unroll
+  for (int q = 0; q < HALVES; ++q)
+#pragma unroll
+    for (int j = 0; j < 4 * OUT; ++j) wscale[q][j] = ws[q * a.n + (c0 + j < a.n ? c0 + j : a.n - 1)];
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = rt.m0 + 16 * (MI * wm + i) + r;
+    const long long src = rt.zero ? -1 : source_row(a, m < rt.m1 ? m : rt.m1 - 1);
+    real[i] = src >= 0;
+    xscale[i] = a.xrows ? a.xs[real[i] ? src : 0] : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    const int m = rt.m0 + 16 * (MI * wm + i) + r;
+    if (m >= rt.m1 || c0 >= a.n) continue;
+    uint8_t* to = a.y + 2 * (m * a.ldy + c0);
+#pragma unroll
+    for (int p = 0; p < OUT; p += 2) {  // 8 columns
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float q = scaled(acc[i][p + j / 4][j % 4], xscale[i], wscale[0][4 * p + j]);
+        v[j] = GATED ? gate(q, scaled(acc[i][NI - OUT + p + j / 4][j % 4], xscale[i], wscale[HALVES - 1][4 * p + j])) : q;
+        if (!real[i]) v[j] = 0.0f;
+      }
+      const u32x4 o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
+      const int c = c0 + 4 * p;
+      if (c + 8 <= a.n) {
+        *reinterpret_cast<u32x4_any*>(to + 8 * p) = o;
+      } else {
+#pragma unroll
+        for (int j = 0; j < 7; ++j)
+          if (c + j < a.n) reinterpret_cast<uint16_t*>(to + 8 * p)[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+      }
+    }
+  }
+}
+
 qr_status launch_product8(int dt, bool gated, const Product8Args& a, hipStream_t st);
 
 }  // namespace qr

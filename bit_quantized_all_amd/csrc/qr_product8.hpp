@@ -35,17 +35,24 @@ __device__ __forceinline__ float scaled(int sum, float xs, float ws) {
 // ---------------------------------------------------------------------------
 
 // One workgroup of KW waves multiplies 16 MF rows of x by 16 NF rows of the
-// weight (gated: NF / 2 fragments of the gate rows and as many of the up rows),
-// each wave a share of the runs of k.  The matrix unit's product is 16 x 16 x 64:
-// lane (r = lane & 15, g = lane >> 4) holds 16 bytes of row r of either side, and
-// which bytes of k they are does not matter as long as both sides have the same.
-// The weight is the unit's A, so that a lane gets four neighbouring columns of
-// one row of y.
+// weight (gated: NF / 2 fragments of the gate rows and as many of the up rows).
+// The waves share the runs of k, wave w has runs w, w + KW, ...; their sums, whole
+// numbers, are added up in LDS in whatever order.  The matrix unit's product is 16
+// x 16 x 64: lane (r = lane & 15, g = lane >> 4) holds 16 bytes of row r of either
+// side, and which bytes of k they are does not matter as long as both sides have
+// the same.  The weight is the unit's A, so that a lane gets four neighbouring
+// columns of one row of y.
+//
+// Fragments come straight from memory, 64 bytes of 16 rows at a time, the next
+// run's while one is multiplied.  The workgroups begin at different runs: rows lie a
+// power of two apart, and if all of them read the same columns of their rows at the
+// same time, they meet in a few of the memory's channels (16 rows, gated, n = k = 8192:
+// 28.2 us and 33.0 on the device; n = k = 8192: 14.1 and 20.9).
 template <int DT, bool GATED, int MF, int NF, int KW>
 __global__ __launch_bounds__(kWave* KW) void fragments8_kernel(Product8Args a) {
   constexpr int HALVES = GATED ? 2 : 1, OUT = NF / HALVES;
   static_assert(OUT * HALVES == NF, "as many gate as up fragments");
-  __shared__ i32x4 sums[KW > 1 ? KW : 1][MF][NF][kWave];
+  __shared__ int sums[MF][NF][4][kWave];
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int r = lane & 15, g = lane >> 4;
@@ -54,84 +61,114 @@ __global__ __launch_bounds__(kWave* KW) void fragments8_kernel(Product8Args a) {
   rt.zero |= a.xrows == 0;  // every row number is out of range then
   const int n0 = (int)(blockIdx.x % a.ntiles) * 16 * OUT;
   const long long row_bytes = (long long)a.blocks * kRowRun;
+  for (int t = threadIdx.x; t < MF * NF * 4 * kWave; t += kWave * KW) (&sums[0][0][0][0])[t] = 0;
 
-  i32x4 acc[MF][NF];
-#pragma unroll
-  for (int i = 0; i < MF; ++i)
-#pragma unroll
-    for (int f = 0; f < NF; ++f) acc[i][f] = i32x4{0, 0, 0, 0};
-  if (!rt.zero) {
-    // rows past the end repeat the last, rows of no source the first of x, columns past the last the last
+  if (!rt.zero && wave < a.blocks) {
+    struct Set {
+      i32x4 w[2][NF], x[2][MF];
+    };
+    // columns past the last repeat it, rows past the end the last, rows of no source the first of x
     const uint8_t *x[MF], *w[NF];
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const int c = n0 + 16 * (f % OUT) + r;
+      w[f] = a.w + (((long long)rt.expert * HALVES + f / OUT) * a.n + (c < a.n ? c : a.n - 1)) * row_bytes + 16 * g;
+    }
+    const int runs = (a.blocks - wave + KW - 1) / KW;
+    const int turn = (int)((blockIdx.x / kXCDs * 0x9E3779B1u >> 16) % (unsigned)runs);
+    auto at = [&](int run) {
+      run += turn;
+      return (size_t)(wave + KW * (run < runs ? run : run - runs)) * kRowRun;
+    };
+    auto load_w = [&](Set& to, int run) {
+#pragma unroll
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) to.w[h][f] = *reinterpret_cast<const i32x4*>(w[f] + at(run) + 64 * h);
+    };
+    auto load_x = [&](Set& to, int run) {
+#pragma unroll
+      for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) to.x[h][i] = *reinterpret_cast<const i32x4*>(x[i] + at(run) + 64 * h);
+    };
+    i32x4 acc[MF][NF];
+#pragma unroll
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+      for (int f = 0; f < NF; ++f) acc[i][f] = i32x4{0, 0, 0, 0};
+    auto multiply = [&](const Set& s) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+#pragma unroll
+          for (int f = 0; f < NF; ++f) acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(s.w[h][f], s.x[h][i], acc[i][f], 0, 0, 0);
+    };
+    Set p, q;
+    // the first weights need not wait for the numbers of the rows of x, which are a trip to memory of their own
+    load_w(p, 0);
 #pragma unroll
     for (int i = 0; i < MF; ++i) {
       const int m = rt.m0 + 16 * i + r;
       const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
       x[i] = a.x + (s < 0 ? 0 : s) * row_bytes + 16 * g;
     }
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const int c = n0 + 16 * (f % OUT) + r;
-      w[f] = a.w + (((long long)rt.expert * HALVES + f / OUT) * a.n + (c < a.n ? c : a.n - 1)) * row_bytes + 16 * g;
+    load_x(p, 0);
+    // no branch around a load, which would make the products before it wait for it
+    int b = 0;
+    for (; b + 2 < runs; b += 2) {
+      load_w(q, b + 1);
+      load_x(q, b + 1);
+      multiply(p);
+      load_w(p, b + 2);
+      load_x(p, b + 2);
+      multiply(q);
     }
-    for (int b = wave; b < a.blocks; b += KW) {
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        i32x4 xv[MF], wv[NF];
-#pragma unroll
-        for (int f = 0; f < NF; ++f) wv[f] = *reinterpret_cast<const i32x4*>(w[f] + (size_t)b * kRowRun + 64 * h);
-#pragma unroll
-        for (int i = 0; i < MF; ++i) xv[i] = *reinterpret_cast<const i32x4*>(x[i] + (size_t)b * kRowRun + 64 * h);
-#pragma unroll
-        for (int i = 0; i < MF; ++i)
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-            acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[f], xv[i], acc[i][f], 0, 0, 0);
-      }
+    if (b + 1 < runs) {
+      load_w(q, b + 1);
+      load_x(q, b + 1);
+      multiply(p);
+      multiply(q);
+    } else {
+      multiply(p);
     }
-  }
-  if constexpr (KW > 1) {
+    __syncthreads();  // sums are zero
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-      for (int f = 0; f < NF; ++f) sums[wave][i][f][lane] = acc[i][f];
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          __hip_atomic_fetch_add(&sums[i][f][j][lane], acc[i][f][j], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_WORKGROUP);
+  } else {
     __syncthreads();
   }
-  // fragment (i, f) of y is joined and stored by wave (i OUT + f) % KW
+  __syncthreads();
+  // fragment (i, f) of y is stored by wave (i OUT + f) % KW
+  for (int frag = wave; frag < MF * OUT; frag += KW) {
+    const int i = frag / OUT, f = frag % OUT;
+    const int m = rt.m0 + 16 * i + r, c = n0 + 16 * f + 4 * g;
+    if (m >= rt.m1 || c >= a.n) continue;
+    const long long src = rt.zero ? -1 : source_row(a, m);
+    const float xs = src >= 0 ? a.xs[src] : 0.0f;
+    const float* ws = a.ws + (long long)(rt.zero ? 0 : rt.expert) * HALVES * a.n + c;
+    float v[4];
 #pragma unroll
-  for (int i = 0; i < MF; ++i) {
+    for (int j = 0; j < 4; ++j) {
+      const int cj = c + j < a.n ? j : a.n - 1 - c;
+      const float p = scaled(sums[i][f][j][lane], xs, ws[cj]);
+      v[j] = GATED ? gate(p, scaled(sums[i][NF - OUT + f][j][lane], xs, ws[(GATED ? a.n : 0) + cj])) : p;
+      if (src < 0) v[j] = 0.0f;
+    }
+    uint8_t* to = a.y + 2 * (m * a.ldy + c);
+    const u32x2 o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
+    if (c + 4 <= a.n) {
+      *reinterpret_cast<u32x2_any*>(to) = o;
+    } else {
 #pragma unroll
-    for (int f = 0; f < OUT; ++f) {
-      if (KW > 1 && (i * OUT + f) % KW != wave) continue;
-      const int m = rt.m0 + 16 * i + r, c = n0 + 16 * f + 4 * g;
-      if (m >= rt.m1 || c >= a.n) continue;
-      i32x4 s[HALVES];
-#pragma unroll
-      for (int h = 0; h < HALVES; ++h) {
-        s[h] = KW > 1 ? sums[0][i][h * OUT + f][lane] : acc[i][h * OUT + f];
-#pragma unroll
-        for (int k = 1; k < KW; ++k) s[h] += sums[k][i][h * OUT + f][lane];
-      }
-      const long long src = rt.zero ? -1 : source_row(a, m);
-      const float xs = src >= 0 ? a.xs[src] : 0.0f;
-      const float* ws = a.ws + (long long)(rt.zero ? 0 : rt.expert) * HALVES * a.n + c;
-      float v[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int cj = c + j < a.n ? j : a.n - 1 - c;
-        const float p = scaled(s[0][j], xs, ws[cj]);
-        v[j] = GATED ? gate(p, scaled(s[HALVES - 1][j], xs, ws[(GATED ? a.n : 0) + cj])) : p;
-        if (src < 0) v[j] = 0.0f;
-      }
-      uint8_t* to = a.y + 2 * (m * a.ldy + c);
-      const u32x2 o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3])};
-      if (c + 4 <= a.n) {
-        *reinterpret_cast<u32x2_any*>(to) = o;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-          if (c + j < a.n) reinterpret_cast<uint16_t*>(to)[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
-      }
+      for (int j = 0; j < 3; ++j)
+        if (c + j < a.n) reinterpret_cast<uint16_t*>(to)[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
     }
   }
 }
@@ -139,6 +176,36 @@ __global__ __launch_bounds__(kWave* KW) void fragments8_kernel(Product8Args a) {
 // ---------------------------------------------------------------------------
 // tiles
 // ---------------------------------------------------------------------------
+
+// Number of row tiles that find_rows() hands out, of groups whose offsets are in order or not: every wave
+// counts them on its own, a lane an expert.
+template <int BM>
+__device__ __forceinline__ int count_tiles(const ProductArgs& a) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int count = 0, top = 0;
+  for (int e0 = 0; e0 <= a.experts; e0 += kWave) {
+    const int e = e0 + lane;  // e == experts: the rows of no expert
+    int lo = a.slots, hi = a.slots;
+    if (e <= a.experts) {
+      lo = clampi(a.offsets[e], 0, a.slots);
+      hi = e < a.experts ? clampi(a.offsets[e + 1], 0, a.slots) : a.slots;
+    }
+    // an offset below an earlier one counts as that one
+    lo = lo > top ? lo : top;
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) {
+      const int o = __shfl_up(lo, s);
+      if (lane >= s && o > lo) lo = o;
+    }
+    hi = hi > lo ? hi : lo;
+    top = __builtin_amdgcn_readlane(hi, kWave - 1);
+    int mine = hi > lo ? (hi - lo + BM - 1) / BM : 0;
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) mine += __shfl_xor(mine, s);
+    count += mine;
+  }
+  return __builtin_amdgcn_readfirstlane(count);
+}
 
 // A workgroup of WM x WN waves computes a tile of 16 WM MI rows of x by 16 WN NI
 // rows of the weight, each wave MI x NI fragments.  A stage is one run of 128
@@ -153,7 +220,7 @@ __global__ __launch_bounds__(kWave* KW) void fragments8_kernel(Product8Args a) {
 // OUT q + 4 f + j, so that a lane has 4 OUT neighbours of a row of y and four
 // lanes a run of it.  Gated: the first half of a wave's fragments are gate rows,
 // the second the same columns' up rows.
-template <int DT, bool GATED, int WM, int WN, int MI, int NI>
+template <int DT, bool GATED, int WM, int WN, int MI, int NI, int NB>
 __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a) {
   constexpr int WAVES = WM * WN, HALVES = GATED ? 2 : 1, OUT = NI / HALVES;
   static_assert(OUT * HALVES == NI, "as many gate as up fragments");
@@ -164,13 +231,16 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
   // are read from LDS kAhead slots before they are multiplied, into a ring; those of the weight a step before.
   constexpr int SLOTS = 2 * MI, kAhead = 3, kRing = 4;
   static_assert(SLOTS % kRing == 0 && MI >= NI && MI > kAhead, "rings begin anew with each stage");
-  __shared__ i32x4 lds[2][BM + BN][8];
+  __shared__ i32x4 lds[NB][BM + BN][8];
 
   const int lane = threadIdx.x & (kWave - 1);
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
-  const TileIndex ti = tile_index(blockIdx.x, gridDim.x, a.ntiles);
+  // The launch is an upper bound on the tiles of groups: those that there are are dealt to the XCDs.
+  const int rows_here = a.offsets ? min(count_tiles<BM>(a) - a.tile0, (int)(gridDim.x / a.ntiles)) : (int)(gridDim.x / a.ntiles);
+  if ((int)blockIdx.x >= rows_here * a.ntiles) return;
+  const TileIndex ti = tile_index(blockIdx.x, rows_here * a.ntiles, a.ntiles);
   RowTile rt = find_rows<BM>(a, a.tile0 + ti.row);
   if (rt.m0 >= rt.m1) return;
   rt.zero |= a.xrows == 0;  // every row number is out of range then
@@ -221,37 +291,38 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
     auto read_w = [&](int buf, int s, int f) { w[s][f] = lds[buf][BM + 16 * (NI * wn + f) + r][(4 * s + g) ^ place(r)]; };
     const int stages = a.blocks;
 #pragma unroll
-    for (int l = 0; l < LOADS; ++l) fetch(0, 0, l);
-    loads_done<0>();
-    stage_barrier();
-    if (stages > 1) {
+    for (int b = 0; b < NB; ++b) {
+      if (b < stages) {
 #pragma unroll
-      for (int l = 0; l < LOADS; ++l) fetch(1, 1, l);
+        for (int l = 0; l < LOADS; ++l) fetch(b, b, l);
+      }
     }
+    if (NB <= stages) loads_done<(NB - 1) * LOADS>(); else loads_done<0>();
+    stage_barrier();
 #pragma unroll
     for (int f = 0; f < NI; ++f) read_w(0, 0, f);
 #pragma unroll
     for (int t = 0; t < kAhead; ++t) read_x(0, t);
-    for (int st = 0; st < stages; ++st) {
-      const int buf = st & 1;
+    for (int st = 0, buf = 0; st < stages; ++st) {
+      const int next = buf + 1 < NB ? buf + 1 : 0;
 #pragma unroll
       for (int t = 0; t < SLOTS; ++t) {
         const int s = t / MI, i = t % MI, left = SLOTS - t;
         if (left == kAhead) {
           // The next stage is there for every wave, and every wave has read the last of this one.
-          loads_done<0>();
+          if (st + NB <= stages) loads_done<(NB - 2) * LOADS>(); else loads_done<0>();
           __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS; a builtin, so that the compiler does not wait once more
           asm volatile("s_barrier" ::: "memory");
         }
         // (after the last stage what lies there is read for nobody)
-        if (left > kAhead) read_x(buf, t + kAhead); else read_x(1 - buf, t + kAhead - SLOTS);
+        if (left > kAhead) read_x(buf, t + kAhead); else read_x(next, t + kAhead - SLOTS);
         if (s == 0 && i < NI) read_w(buf, 1, i);
         if (left <= kAhead) {
 #pragma unroll
-          for (int f = NI * (kAhead - left) / kAhead; f < NI * (kAhead - left + 1) / kAhead; ++f) read_w(1 - buf, 0, f);
-          if (st + 2 < stages) {
+          for (int f = NI * (kAhead - left) / kAhead; f < NI * (kAhead - left + 1) / kAhead; ++f) read_w(next, 0, f);
+          if (st + NB < stages) {
 #pragma unroll
-            for (int l = LOADS * (kAhead - left) / kAhead; l < LOADS * (kAhead - left + 1) / kAhead; ++l) fetch(st + 2, buf, l);
+            for (int l = LOADS * (kAhead - left) / kAhead; l < LOADS * (kAhead - left + 1) / kAhead; ++l) fetch(st + NB, buf, l);
           }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -259,6 +330,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
         for (int f = 0; f < NI; ++f) acc[i][f] = __builtin_amdgcn_mfma_i32_16x16x64_i8(w[s][f], x[t % kRing], acc[i][f], 0, 0, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
+      buf = next;
     }
   }
 
@@ -283,24 +355,40 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
     const int m = rt.m0 + 16 * (MI * wm + i) + r;
     if (m >= rt.m1 || c0 >= a.n) continue;
     uint8_t* to = a.y + 2 * (m * a.ldy + c0);
+    uint16_t o[4 * OUT];
 #pragma unroll
-    for (int p = 0; p < OUT; p += 2) {  // 8 columns
-      float v[8];
+    for (int p = 0; p < OUT; ++p) {
+      float v[4];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float q = scaled(acc[i][p + j / 4][j % 4], xscale[i], wscale[0][4 * p + j]);
-        v[j] = GATED ? gate(q, scaled(acc[i][NI - OUT + p + j / 4][j % 4], xscale[i], wscale[HALVES - 1][4 * p + j])) : q;
+      for (int j = 0; j < 4; ++j) {
+        const float q = scaled(acc[i][p][j], xscale[i], wscale[0][4 * p + j]);
+        v[j] = GATED ? gate(q, scaled(acc[i][NI - OUT + p][j], xscale[i], wscale[HALVES - 1][4 * p + j])) : q;
         if (!real[i]) v[j] = 0.0f;
       }
-      const u32x4 o = {pack2<DT>(v[0], v[1]), pack2<DT>(v[2], v[3]), pack2<DT>(v[4], v[5]), pack2<DT>(v[6], v[7])};
-      const int c = c0 + 4 * p;
-      if (c + 8 <= a.n) {
-        *reinterpret_cast<u32x4_any*>(to + 8 * p) = o;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const uint32_t two = pack2<DT>(v[2 * j], v[2 * j + 1]);
+        o[4 * p + 2 * j] = (uint16_t)two;
+        o[4 * p + 2 * j + 1] = (uint16_t)(two >> 16);
+      }
+    }
+    if (c0 + 4 * OUT <= a.n) {
+      if constexpr (OUT == 1) {
+        u32x2 v;
+        __builtin_memcpy(&v, o, 8);
+        *reinterpret_cast<u32x2_any*>(to) = v;
       } else {
 #pragma unroll
-        for (int j = 0; j < 7; ++j)
-          if (c + j < a.n) reinterpret_cast<uint16_t*>(to + 8 * p)[j] = (uint16_t)(o[j >> 1] >> (16 * (j & 1)));
+        for (int p = 0; p < OUT; p += 2) {
+          u32x4 v;
+          __builtin_memcpy(&v, o + 4 * p, 16);
+          *reinterpret_cast<u32x4_any*>(to + 8 * p) = v;
+        }
       }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4 * OUT - 1; ++j)
+        if (c0 + j < a.n) reinterpret_cast<uint16_t*>(to)[j] = o[j];
     }
   }
 }

@@ -237,12 +237,33 @@ __device__ __forceinline__ void first_largest(double& v, int& at) {
   }
 }
 
-// A wave chooses for one token.
+// The gate of a chosen expert with logit l (-inf: none), `base` the row's largest logit where p is not
+// renormalised.  LARGEST and SUM go over the lanes that hold the token's chosen.
+//
+// sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).  Renormalised, every score may take the same factor, so that
+// those of the chosen do not vanish together: the largest of them has exp(0).
+template <typename LARGEST, typename SUM>
+__device__ __forceinline__ float gate_of(const ChooseArgs& a, float l, float base, float sum, LARGEST largest_of,
+                                         SUM sum_of) {
+  const float none = -__builtin_inff();
+  const float low = a.sigmoid ? fminf(l, 0.0f) : l;
+  if (a.renormalise)
+    base = largest_of(low);
+  else if (a.sigmoid)
+    base = 0.0f;
+  float p = l > none ? expf(low - base) : 0.0f;
+  if (a.sigmoid) p /= 1.0f + expf(-fabsf(l));
+  if (a.renormalise)
+    p /= sum_of(p);
+  else if (!a.sigmoid)
+    p /= sum;
+  return l > none ? p * a.factor : 0.0f;
+}
+
+// A wave chooses for one token, with ranks in 64 bits.
 template <int DT>
-__global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
-  __shared__ double ranks[QR_MAX_EXPERTS];
-  const long long t = blockIdx.x;
-  const int lane = threadIdx.x;
+__device__ __forceinline__ void choose_token(const ChooseArgs& a, long long t, double* ranks) {
+  const int lane = threadIdx.x & (kWave - 1);
   const float none = -__builtin_inff();
   float largest = none;
   for (int e = lane; e < a.experts; e += kWave) largest = fmaxf(largest, logit<DT>(a, t, e));
@@ -252,21 +273,23 @@ __global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
     for (int e = lane; e < a.experts; e += kWave) sum += exp((double)logit<DT>(a, t, e) - (double)largest);
     for (int s = 1; s < kWave; s <<= 1) sum += __shfl_xor(sum, s);
   }
+  const bool by_score = a.bias || (a.best == 2 && a.groups > 1);
   for (int e = lane; e < a.experts; e += kWave) {
     const float l = logit<DT>(a, t, e);
-    double p = 0.0, rank = none;
+    double rank = none;
     if (l > none) {
-      p = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)largest) / sum;
-      // without a bias in the order of the logits
-      const double r = a.bias ? p + (double)a.bias[e] : a.best == 2 && a.groups > 1 ? p : (double)l;
-      rank = r > none ? r : (double)none;  // a bias of NaN
+      rank = (double)l;
+      if (by_score) {
+        const double p = a.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)largest) / sum;
+        const double r = a.bias ? p + (double)a.bias[e] : p;
+        rank = r > none ? r : (double)none;  // a bias of NaN
+      }
     }
     ranks[e] = rank;
   }
-  __syncthreads();
-  unsigned long long kept = ~0ull;
-  const int each = a.experts / a.groups;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if (a.groups > 1) {
+    const int each = a.experts / a.groups;
     double value = none;
     if (lane < a.groups) {
       double first = none, second = none;
@@ -281,7 +304,7 @@ __global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
       }
       value = a.best == 2 && second > none ? first + second : first;
     }
-    kept = 0;
+    unsigned long long kept = 0;
     for (int j = 0; j < a.top_groups; ++j) {
       double v = value;
       int g = lane;
@@ -290,13 +313,15 @@ __global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
       kept |= 1ull << g;
       if (g == lane) value = none;
     }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    for (int e = lane; e < a.experts; e += kWave) {
+      if (!(kept >> (e / each) & 1))
+        ranks[e] = none;
+      else if (!a.bias && ranks[e] > none)
+        ranks[e] = (double)logit<DT>(a, t, e);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  __syncthreads();
-  for (int e = lane; e < a.experts; e += kWave) {
-    if (!(kept >> (a.groups > 1 ? e / each : 0) & 1)) ranks[e] = none;
-    else if (!a.bias && ranks[e] > none) ranks[e] = (double)logit<DT>(a, t, e);
-  }
-  __syncthreads();
   int mine = -1;  // lane j has the j-th expert
   for (int j = 0; j < a.top; ++j) {
     double v = none;
@@ -311,29 +336,297 @@ __global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
     if (!(v > none)) break;
     if (lane == j) mine = at;
     if (lane == at % kWave) ranks[at] = none;
-    __syncthreads();
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   }
-  // sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).  Renormalised, every score may take the same
-  // factor, so that those of the chosen do not vanish together: the largest of them has exp(0).
-  const float l = mine >= 0 ? logit<DT>(a, t, mine) : none;
-  const float low = a.sigmoid ? fminf(l, 0.0f) : l;
-  float base = a.sigmoid ? 0.0f : largest;
-  if (a.renormalise) {
-    base = low;
-    for (int s = 1; s < kWave; s <<= 1) base = fmaxf(base, __shfl_xor(base, s));
-  }
-  float p = mine >= 0 ? expf(low - base) : 0.0f;
-  if (a.sigmoid) p /= 1.0f + expf(-fabsf(l));
-  if (a.renormalise) {
-    float total = p;
-    for (int s = 1; s < kWave; s <<= 1) total += __shfl_xor(total, s);
-    p /= total;
-  } else if (!a.sigmoid) {
-    p /= (float)sum;
-  }
+  const float gate = gate_of(
+      a, mine >= 0 ? logit<DT>(a, t, mine) : none, largest, (float)sum,
+      [](float v) {
+        for (int s = 1; s < kWave; s <<= 1) v = fmaxf(v, __shfl_xor(v, s));
+        return v;
+      },
+      [](float v) {
+        for (int s = 1; s < kWave; s <<= 1) v += __shfl_xor(v, s);
+        return v;
+      });
   if (lane < a.top) {
     a.ids[t * a.top + lane] = mine;
-    a.gates[t * a.top + lane] = mine >= 0 ? p * a.factor : 0.0f;
+    a.gates[t * a.top + lane] = gate;
+  }
+}
+
+template <int DT>
+__global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
+  __shared__ double ranks[QR_MAX_EXPERTS];
+  choose_token<DT>(a, blockIdx.x, ranks);
+}
+
+// A row of 16 lanes chooses for one token, a lane holding the ranks of V neighbouring experts in registers, in
+// fp32.  Ranks, and groups' values, that are nearer to each other than fp32 may be off leave the choice open; the
+// wave then takes the same steps in 64 bits.  (Without a bias the logits are compared, which is exact.)
+constexpr int kChooseLanes = 16, kChooseThreads = 256;
+
+template <int N>
+__device__ __forceinline__ float row_ror(float v) {
+  return __builtin_bit_cast(float, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), 0x120 + N, 0xF, 0xF, true));
+}
+template <int N>
+__device__ __forceinline__ double row_ror(double v) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  i32x2 w = __builtin_bit_cast(i32x2, v);
+  w.x = __builtin_amdgcn_mov_dpp(w.x, 0x120 + N, 0xF, 0xF, true);
+  w.y = __builtin_amdgcn_mov_dpp(w.y, 0x120 + N, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, w);
+}
+__device__ __forceinline__ float larger(float a, float b) { return fmaxf(a, b); }
+__device__ __forceinline__ double larger(double a, double b) { return fmax(a, b); }
+__device__ __forceinline__ float smaller(float a, float b) { return fminf(a, b); }
+__device__ __forceinline__ double smaller(double a, double b) { return fmin(a, b); }
+template <typename K>
+__device__ __forceinline__ K row_max(K v) {
+  v = larger(v, row_ror<8>(v));
+  v = larger(v, row_ror<4>(v));
+  v = larger(v, row_ror<2>(v));
+  return larger(v, row_ror<1>(v));
+}
+// (The same bits in every lane: each step adds two values in one or the other order.)
+template <typename K>
+__device__ __forceinline__ K row_sum(K v) {
+  v += row_ror<8>(v);
+  v += row_ror<4>(v);
+  v += row_ror<2>(v);
+  return v + row_ror<1>(v);
+}
+
+// V neighbouring values of a row of `n` from value V lane on, `fill` past the end.
+template <int DT, int V>
+__device__ __forceinline__ void load_run(const uint8_t* row, int lane, int n, float fill, float (&k)[V]) {
+  constexpr int BYTES = DT == 2 ? 4 : 2, PER = V * BYTES >= 16 ? 16 / BYTES : V;  // values of one load
+  typedef uint32_t words __attribute__((ext_vector_type(PER * BYTES >= 4 ? PER * BYTES / 4 : 1), aligned(BYTES)));
+  if (PER * BYTES >= 4 && n % V == 0) {
+    if (V * lane < n) {
+#pragma unroll
+      for (int q = 0; q < V / PER; ++q) {
+        const words w = *reinterpret_cast<const words*>(row + (V * lane + PER * q) * BYTES);
+#pragma unroll
+        for (int i = 0; i < PER; ++i) {
+          if constexpr (DT == 2)
+            k[PER * q + i] = __builtin_bit_cast(float, (uint32_t)w[i]);
+          else
+            k[PER * q + i] = i & 1 ? hi_to_f32<DT == 2 ? 0 : DT>(w[i / 2]) : lo_to_f32<DT == 2 ? 0 : DT>(w[i / 2]);
+        }
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) k[v] = fill;
+    }
+    return;
+  }
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    const int e = V * lane + v < n ? V * lane + v : n - 1;
+    float x;
+    if constexpr (DT == 2)
+      x = reinterpret_cast<const float*>(row)[e];
+    else
+      x = lo_to_f32<DT == 2 ? 0 : DT>(reinterpret_cast<const uint16_t*>(row)[e]);
+    k[v] = V * lane + v < n ? x : fill;
+  }
+}
+
+// The row's choice from its logits l (clamped, -inf: out), into chosen[0 .. top - 1] in LDS, -1 for none; `sum` of
+// the softmax where it is needed.  Returns whether it is open (K = float only).
+template <typename K, int V, typename LOGIT>
+__device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (&l)[V], float largest, float& sum,
+                                              int* chosen, LOGIT logit_at) {
+  constexpr bool kExact = sizeof(K) == 8;
+  const int lane = threadIdx.x & (kChooseLanes - 1), row = (threadIdx.x & (kWave - 1)) / kChooseLanes;
+  const K none = -__builtin_inff();
+  const bool by_score = a.bias || (a.best == 2 && a.groups > 1);
+  K k[V], total = 0;
+  if (by_score || (!a.sigmoid && !a.renormalise && !kExact)) {
+    // (-inf times 0 is NaN, which larger() takes for none)
+    if (a.sigmoid) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (kExact)
+          k[v] = 1.0 / (1.0 + exp(-(double)l[v]));
+        else
+          k[v] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[v]));
+        k[v] = larger(k[v] + (K)(l[v] * 0.0f), none);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        if constexpr (kExact)
+          k[v] = l[v] > -__builtin_inff() ? exp((double)l[v] - (double)largest) : 0.0;
+        else
+          k[v] = l[v] > -__builtin_inff() ? __expf(l[v] - largest) : 0.0f;
+        total += k[v];
+      }
+      total = row_sum(total);
+      sum = (float)total;
+#pragma unroll
+      for (int v = 0; v < V; ++v) k[v] = larger(k[v] / total + (K)(l[v] * 0.0f), none);
+    }
+  }
+  bool open = false;
+  // What two ranks may be off together, and as much again.  sigmoid: the exponential's argument and value are off
+  // by (|l| + 2) 2^-23, of which p (1 - p) <= 1 / 4, and p (1 - p) |l| < 1 / 4, come through; the sum and the
+  // reciprocal by 2^-23 and 2^-24 of p: in all below 2^-22.  softmax: the exponential by (d + 2) 2^-23 of it, d the
+  // distance to the largest logit, p d < 1 / 2 of the largest p; the sum by that on average, where d < 7, and V + 4
+  // steps; the quotient by two: (V + 32) 2^-24 of the largest p.  The sum with the bias by half a step.
+  const float slack = a.sigmoid ? 0x1p-20f : (V + 32) * 0x1p-22f / sum;
+  if (a.bias) {
+    float b[V];
+    load_run<2, V>(reinterpret_cast<const uint8_t*>(a.bias), lane, a.experts, 0.0f, b);
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = larger(k[v] + (K)b[v], none);  // a bias of NaN: none
+  }
+  if (a.groups > 1) {
+    const int span = a.experts / a.groups / V;  // lanes of a group
+    K one = none, two = none;                   // the largest ranks of the lane, of the group
+    if (by_score) {
+#pragma unroll
+      for (int v = 0; v < V; ++v) {
+        two = larger(two, smaller(one, k[v]));
+        one = larger(one, k[v]);
+      }
+    } else {
+#pragma unroll
+      for (int v = 0; v < V; ++v) one = larger(one, (K)l[v]);
+    }
+    for (int s = 1; s < span; s <<= 1) {
+      const K o = __shfl_xor(one, s), w = __shfl_xor(two, s);
+      two = larger(larger(two, w), smaller(one, o));
+      one = larger(one, o);
+    }
+    const K value = a.best == 2 && two > none ? one + two : one;
+    // a group is kept if fewer than top_groups come before it; two values may be off by twice as much as two ranks
+    const K near_by = 2.0f * slack + 0x1p-20f * (float)value;
+    int before = 0;
+    bool near = false;
+    const int group = lane / span;
+    for (int g = 0; g < a.groups; ++g) {
+      const K o = __shfl(value, (threadIdx.x & 48) + g * span);
+      before += o > value || (o == value && g < group);
+      if (!kExact) near |= g != group && fabsf((float)(value - o)) <= near_by;
+    }
+    const bool kept = before < a.top_groups && value > none;
+    if (!kExact) open = by_score && before == a.top_groups - 1 && near;
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = kept ? a.bias ? k[v] : (K)l[v] : none;
+  } else if (!a.bias) {
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = l[v];
+  }
+  chosen[lane] = -1;
+  K last = 0;
+  // With a bias, in fp32, it goes on until a rank is clearly below the one before it, and the top-th at least.
+  const bool ahead = a.bias && !kExact;
+  bool done = false, sort = false;
+  int count = 0;
+  for (int j = 0; j < (ahead ? kChooseLanes : a.top); ++j) {
+    K m = k[0];
+#pragma unroll
+    for (int v = 1; v < V; ++v) m = larger(m, k[v]);
+    const K most = row_max(m);
+    done |= !(most > none);
+    if (ahead) {
+      // (NaN, of two ranks of +inf, is not clear)
+      const bool clear = (float)(last - most) > slack + 0x1p-21f * fabsf((float)most);
+      done |= j >= a.top && clear;
+      sort |= !done && j && !clear;
+      last = most;
+    }
+    if (__all(done)) break;
+    // the first of the row's lanes that has it, and there the first
+    const uint32_t has = (uint32_t)(__ballot(m == most && !done) >> (16 * row)) & 0xffffu;
+    const bool mine = (int)__builtin_ctz(has | 0x10000u) == lane;
+    bool found = !mine;
+    int at = 0;
+#pragma unroll
+    for (int v = 0; v < V; ++v) {
+      const bool this_one = !found && k[v] == most;
+      at = this_one ? v : at;
+      k[v] = this_one ? none : k[v];
+      found |= this_one;
+    }
+    if (mine) chosen[j] = V * lane + at;
+    count += !done;
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  if constexpr (!kExact) {
+    if (ahead && count == kChooseLanes && a.experts > kChooseLanes && !done) open = true;  // nothing clearly below was seen
+    if (__any(sort && !open)) {
+      // Lane j takes the j-th of those seen to 64 bits, and its place among them is the number that come before it.
+      double all = 0.0;
+      if (!a.sigmoid) {
+#pragma unroll 1
+        for (int v = 0; v < V; ++v) all += lane * V + v < a.experts && logit_at(lane * V + v) > -__builtin_inff() ? exp((double)logit_at(lane * V + v) - (double)largest) : 0.0;
+        all = row_sum(all);
+      }
+      const int id = chosen[lane];
+      double rank = -__builtin_inf();
+      if (id >= 0) {
+        const double x = logit_at(id);
+        rank = (a.sigmoid ? 1.0 / (1.0 + exp(-x)) : exp(x - (double)largest) / all) + (double)a.bias[id];
+      }
+      int before = 0;
+      for (int q = 0; q < kChooseLanes; ++q) {
+        const double o = __shfl(rank, (threadIdx.x & 48) + q);
+        const int e = __shfl(id, (threadIdx.x & 48) + q);
+        before += e >= 0 && (o > rank || (o == rank && e < id));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      if (id >= 0 && sort) chosen[before] = id;
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    }
+  }
+  return open;
+}
+
+template <int DT, int V>
+__global__ __launch_bounds__(kChooseThreads) void choose_rows_kernel(ChooseArgs a) {
+  constexpr int WAVES = kChooseThreads / kWave, ROWS = kWave / kChooseLanes;
+  __shared__ int lds[WAVES][ROWS][kChooseLanes];
+  const float none = -__builtin_inff();
+  const int wave = threadIdx.x / kWave, row = (threadIdx.x & (kWave - 1)) / kChooseLanes;
+  const int lane = threadIdx.x & (kChooseLanes - 1);  // of the row
+  const long long first = ((long long)blockIdx.x * WAVES + wave) * ROWS, t = first + row;
+  if (first >= a.tokens) return;
+  const bool here = t < a.tokens;
+
+  float l[V], largest = none, sum = 1.0f;
+  load_run<DT, V>(a.logits + (DT == 2 ? 4 : 2) * (here ? t : (long long)a.tokens - 1) * a.ldl, lane, a.experts, none, l);
+#pragma unroll
+  for (int v = 0; v < V; ++v) {
+    l[v] = fminf(larger(l[v], none), 3.402823466e38f);  // NaN: -inf
+    largest = larger(largest, l[v]);
+  }
+  largest = row_max(largest);
+  int* chosen = lds[wave][row];
+  auto logit_at = [&](int e) { return logit<DT>(a, here ? t : (long long)a.tokens - 1, e); };
+  if (__any(choose_in_row<float, V>(a, l, largest, sum, chosen, logit_at) && here))
+    choose_in_row<double, V>(a, l, largest, sum, chosen, logit_at);
+  if (!here) return;
+  const int mine = lane < a.top ? chosen[lane] : -1;
+  const float gate = gate_of(a, mine >= 0 ? logit<DT>(a, t, mine) : none, largest, sum, row_max<float>, row_sum<float>);
+  if (lane < a.top) {
+    a.ids[t * a.top + lane] = mine;
+    a.gates[t * a.top + lane] = gate;
+  }
+}
+
+template <int DT>
+static auto choose_kernel_of(int run) -> void (*)(ChooseArgs) {
+  switch (run) {
+    case 1: return choose_rows_kernel<DT, 1>;
+    case 2: return choose_rows_kernel<DT, 2>;
+    case 4: return choose_rows_kernel<DT, 4>;
+    case 8: return choose_rows_kernel<DT, 8>;
+    case 16: return choose_rows_kernel<DT, 16>;
+    case 32: return choose_rows_kernel<DT, 32>;
+    default: return choose_kernel<DT>;
   }
 }
 
@@ -563,16 +856,21 @@ qr_status qr_choose(qr_dtype dtype, qr_score score, const void* logits, size_t l
   args.sigmoid = score == QR_SIGMOID;
   args.renormalise = renormalise != 0;
   args.factor = factor;
-  return in_launches((long long)tokens, 1, kWave, [&](long long first, long long count) {
+  // Rows of 16 lanes hold up to 512 experts, in runs of which groups are whole ones.
+  const int each = args.experts / args.groups;
+  int run = 1;
+  while (kChooseLanes * run < args.experts) run <<= 1;
+  const int span = each / run;
+  const bool in_rows = top <= kChooseLanes && run <= 32 && (groups == 1 || (each % run == 0 && (span & (span - 1)) == 0));
+  const int per = in_rows ? kChooseThreads / kChooseLanes : 1, threads = in_rows ? kChooseThreads : kWave;
+  return in_launches((long long)tokens, per, threads, [&](long long first, long long count) {
     ChooseArgs a = args;
     a.logits += width * first * a.ldl;
     a.gates += first * a.top;
     a.ids += first * a.top;
     a.tokens = (int)count;
-    return launch_1d(dtype == QR_FP16   ? choose_kernel<kFp16>
-                     : dtype == QR_BF16 ? choose_kernel<kBf16>
-                                        : choose_kernel<2>,
-                     count, kWave, (hipStream_t)stream, a);
+    auto kernel = dtype == QR_FP16 ? choose_kernel_of<kFp16> : dtype == QR_BF16 ? choose_kernel_of<kBf16> : choose_kernel_of<2>;
+    return launch_1d(kernel(in_rows ? run : 0), (count + per - 1) / per, threads, (hipStream_t)stream, a);
   });
 }
 

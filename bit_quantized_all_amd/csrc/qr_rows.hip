@@ -209,6 +209,7 @@ struct ChooseArgs {
   int32_t* ids;
   long long ldl;
   int tokens, experts, top, groups, top_groups, best;
+  int span_bits;  // log2 of the lanes that hold a group (choose_rows_kernel)
   bool sigmoid, renormalise;
   float factor;
 };
@@ -252,7 +253,7 @@ __device__ __forceinline__ float gate_of(const ChooseArgs& a, float l, float bas
   else if (a.sigmoid)
     base = 0.0f;
   float p = l > none ? expf(low - base) : 0.0f;
-  if (a.sigmoid) p /= 1.0f + expf(-fabsf(l));
+  if (a.sigmoid) p *= __builtin_amdgcn_rcpf(1.0f + expf(-fabsf(l)));
   if (a.renormalise)
     p /= sum_of(p);
   else if (!a.sigmoid)
@@ -483,8 +484,7 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
     for (int v = 0; v < V; ++v) k[v] = larger(k[v] + (K)b[v], none);  // a bias of NaN: none
   }
   if (a.groups > 1) {
-    const int span = a.experts / a.groups / V;  // lanes of a group
-    K one = none, two = none;                   // the largest ranks of the lane, of the group
+    K one = none, two = none;  // the largest ranks of the lane, of the group
     if (by_score) {
 #pragma unroll
       for (int v = 0; v < V; ++v) {
@@ -495,22 +495,31 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
 #pragma unroll
       for (int v = 0; v < V; ++v) one = larger(one, (K)l[v]);
     }
-    for (int s = 1; s < span; s <<= 1) {
-      const K o = __shfl_xor(one, s), w = __shfl_xor(two, s);
+    for (int s = 0; s < a.span_bits; ++s) {
+      const K o = __shfl_xor(one, 1 << s), w = __shfl_xor(two, 1 << s);
       two = larger(larger(two, w), smaller(one, o));
       one = larger(one, o);
     }
     const K value = a.best == 2 && two > none ? one + two : one;
-    // a group is kept if fewer than top_groups come before it; two values may be off by twice as much as two ranks
-    const K near_by = 2.0f * slack + 0x1p-20f * (float)value;
+    // A group is kept if fewer than top_groups come before it, counted by their lanes; two values may be off by
+    // twice as much as two ranks.
+    const float near_by = 2.0f * slack + 0x1p-20f * (float)value;
     int before = 0;
     bool near = false;
-    const int group = lane / span;
-    for (int g = 0; g < a.groups; ++g) {
-      const K o = __shfl(value, (threadIdx.x & 48) + g * span);
-      before += o > value || (o == value && g < group);
-      if (!kExact) near |= g != group && fabsf((float)(value - o)) <= near_by;
-    }
+    const int group = lane >> a.span_bits;
+    auto look = [&](auto N) {
+      const K o = row_ror<decltype(N)::value>(value);
+      const int other = ((lane - decltype(N)::value) & (kChooseLanes - 1)) >> a.span_bits;
+      before += o > value || (o == value && other < group);
+      if (!kExact) near |= other != group && fabsf((float)(value - o)) <= near_by;
+    };
+    auto all = [&](auto... n) { (look(n), ...); };
+    all(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{},
+        std::integral_constant<int, 4>{}, std::integral_constant<int, 5>{}, std::integral_constant<int, 6>{},
+        std::integral_constant<int, 7>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 9>{},
+        std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{}, std::integral_constant<int, 12>{},
+        std::integral_constant<int, 13>{}, std::integral_constant<int, 14>{}, std::integral_constant<int, 15>{});
+    before >>= a.span_bits;
     const bool kept = before < a.top_groups && value > none;
     if (!kExact) open = by_score && before == a.top_groups - 1 && near;
 #pragma unroll
@@ -865,6 +874,7 @@ qr_status qr_choose(qr_dtype dtype, qr_score score, const void* logits, size_t l
   const int per = in_rows ? kChooseThreads / kChooseLanes : 1, threads = in_rows ? kChooseThreads : kWave;
   return in_launches((long long)tokens, per, threads, [&](long long first, long long count) {
     ChooseArgs a = args;
+    for (int s = span; s > 1; s >>= 1) ++a.span_bits;
     a.logits += width * first * a.ldl;
     a.gates += first * a.top;
     a.ids += first * a.top;

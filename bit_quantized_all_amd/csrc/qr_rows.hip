@@ -89,8 +89,127 @@ __device__ __forceinline__ uint32_t code(float v, const CodeFactors& f) {
   return f.inverse == 0.0f ? 0u : (uint32_t)(int)fminf(fmaxf(rintf(v * f.up * f.inverse), -127.0f), 127.0f) & 0xffu;
 }
 
+// Values 8 c .. 8 c + 7 of a row of k, without a branch that lanes part at: chunks past the last are zero.
+template <int DT>
+__device__ __forceinline__ u32x4 load_chunk(const uint8_t* row, int c, int chunks, int k) {
+  if (k % 8) return load_x8_tail(row, 8 * c, k);
+  const u32x4 v = *reinterpret_cast<const u32x4_any*>(row + 16 * (size_t)(c < chunks ? c : chunks - 1));
+  return c < chunks ? v : u32x4{0u, 0u, 0u, 0u};
+}
+
+// W waves hold a row in registers, C chunks of 8 values a lane.
+template <int DT, bool NORM, int W, int C>
+__global__ __launch_bounds__(W > 4 ? kWave * W : kRowThreads) void rows_kernel(RowArgs a) {
+  constexpr int ROWS = W < 4 ? 4 / W : 1, LANES = kWave * W;
+  __shared__ float lds[ROWS][W];
+  __shared__ uint32_t lds_bits[ROWS][W];
+  const int group = W < 4 ? threadIdx.x / LANES : 0, lane = threadIdx.x % LANES;
+  const long long row = (long long)blockIdx.x * ROWS + group;
+  const bool here = ROWS == 1 || row < a.rows;  // (a workgroup's waves meet at no barrier where it has several rows)
+  if (!here) return;
+  const int chunks = (a.k + 7) / 8;
+  u32x4 xv[C], rv[C];
+#pragma unroll
+  for (int i = 0; i < C; ++i) xv[i] = load_chunk<DT>(a.x + 2 * row * a.ldx, LANES * i + lane, chunks, a.k);
+  if (NORM && a.residual) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) rv[i] = load_chunk<DT>(a.residual + 2 * row * a.ldr, LANES * i + lane, chunks, a.k);
+  }
+  float h[C][8];
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      h[i][2 * j] = lo_to_f32<DT>(xv[i][j]);
+      h[i][2 * j + 1] = hi_to_f32<DT>(xv[i][j]);
+    }
+  auto over_row = [&](auto v, auto op, auto& shared) {
+#pragma unroll
+    for (int s = 1; s < kWave; s <<= 1) v = op(v, __shfl_xor(v, s));
+    if constexpr (W > 1) {
+      if (lane % kWave == 0) shared[group][lane / kWave] = v;
+      __syncthreads();
+      v = shared[group][0];
+#pragma unroll
+      for (int w = 1; w < W; ++w) v = op(v, shared[group][w]);
+    }
+    return v;
+  };
+  if constexpr (NORM) {
+    if (a.residual) {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          h[i][2 * j] += lo_to_f32<DT>(rv[i][j]);
+          h[i][2 * j + 1] += hi_to_f32<DT>(rv[i][j]);
+        }
+      if (a.total) {
+#pragma unroll
+        for (int i = 0; i < C; ++i)
+          if (LANES * i + lane < chunks) store_values<DT>(a.total + 2 * row * a.ldt, LANES * i + lane, a.k, h[i]);
+      }
+    }
+    u32x4 wv[C];
+#pragma unroll
+    for (int i = 0; i < C; ++i) wv[i] = load_chunk<DT>(a.weight, LANES * i + lane, chunks, a.k);
+    auto squares = [&](float up) {
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[i][j] * up, h[i][j] * up, sum);
+      return over_row(sum, [](float p, float q) { return p + q; }, lds);
+    };
+    float up = 1.0f, mean = squares(1.0f) / (float)a.k;
+    // squares that leave the range of fp32 above or below: once more, scaled
+    if (mean == __builtin_inff())
+      up = 0x1p-80f;
+    else if (mean + a.eps < 0x1p-80f)
+      up = 0x1p90f;
+    if (up != 1.0f) {
+      if constexpr (W > 1) __syncthreads();  // everyone has read the first sum
+      mean = squares(up) / (float)a.k;
+    }
+    const float down = 1.0f / sqrtf(mean + a.eps * up * up);
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[i][2 * j] = h[i][2 * j] * up * down * lo_to_f32<DT>(wv[i][j]);
+        h[i][2 * j + 1] = h[i][2 * j + 1] * up * down * hi_to_f32<DT>(wv[i][j]);
+      }
+    if (a.y) {
+#pragma unroll
+      for (int i = 0; i < C; ++i)
+        if (LANES * i + lane < chunks) store_values<DT>(a.y + 2 * row * a.ldy, LANES * i + lane, a.k, h[i]);
+    }
+    if (!a.codes) return;
+  }
+  uint32_t largest = 0;
+#pragma unroll
+  for (int i = 0; i < C; ++i)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      // of two magnitudes the larger bits are the larger value, and those of infinity and NaN are larger still
+      const uint32_t bits = __builtin_bit_cast(uint32_t, h[i][j]) & 0x7fffffffu;
+      largest = bits > largest ? bits : largest;
+    }
+  const CodeFactors cf = code_factors(over_row(largest, [](uint32_t p, uint32_t q) { return p > q ? p : q; }, lds_bits));
+  if (lane == 0) a.scales[row] = cf.scale;
+#pragma unroll
+  for (int i = 0; i < C; ++i) {
+    const int c = LANES * i + lane;
+    uint32_t q[2] = {0, 0};
+#pragma unroll
+    for (int j = 0; j < 8; ++j) q[j >> 2] |= code(h[i][j], cf) << (8 * (j & 3));
+    if (8 * c < a.row_bytes) *reinterpret_cast<u32x2*>(a.codes + row * a.row_bytes + 8 * c) = u32x2{q[0], q[1]};
+  }
+}
+
+// Rows that are longer than registers hold: read once for each of the squares, the largest value and the result.
 template <int DT, bool NORM>
-__global__ __launch_bounds__(kRowThreads) void rows_kernel(RowArgs a) {
+__global__ __launch_bounds__(kRowThreads) void long_rows_kernel(RowArgs a) {
   __shared__ float lds[kRowThreads / kWave];
   __shared__ uint32_t lds_bits[kRowThreads / kWave];
   const long long row = blockIdx.x;
@@ -121,9 +240,9 @@ __global__ __launch_bounds__(kRowThreads) void rows_kernel(RowArgs a) {
     float mean = squares(1.0f) / (float)a.k;
     // squares that leave the range of fp32 above or below: once more, scaled
     if (mean == __builtin_inff())
-      nf.up = 0x1p-70f;
+      nf.up = 0x1p-80f;
     else if (mean + a.eps < 0x1p-80f)
-      nf.up = 0x1p60f;
+      nf.up = 0x1p90f;
     if (nf.up != 1.0f) mean = squares(nf.up) / (float)a.k;
     nf.down = 1.0f / sqrtf(mean + a.eps * nf.up * nf.up);
   }
@@ -657,8 +776,50 @@ static qr_status in_launches(long long rows, int per, int threads, LAUNCH launch
   return QR_OK;
 }
 
+// How a row is shared out: by W waves of C chunks a lane, a workgroup of fewer than four waves holding several.
+// Two chunks a lane, one where there are few rows, and as few waves as that takes (us, bf16 with a residual, W x C):
+//   1 x 4096              1x8 6.8    4x2 3.4    16x1 3.0
+//   16 x 8192             4x4 4.8    16x1 3.5
+//   1000 x 2048           1x4 7.0    4x1 4.6    16x1 7.9
+//   65536 x 1024          1x2 52     4x1 83     16x1 270     (without a residual)
+//   32768 x 4096          1x8 235    4x2 189    16x1 245
+//   8192 x 8192, 8 bits   4x4 136    16x1 129
+// Rows of over 32768 values are read again for each of a norm's steps.
+struct RowShape {
+  int waves, chunks, rows, threads;  // rows: of a workgroup; waves == 0: long rows
+};
+static RowShape row_shape(long long rows, int k) {
+  const int most = rows <= 512 ? 1 : 2;
+  const int w = k <= 512 * most ? 1 : k <= 2048 * most ? 4 : 16;
+  int c = 1;
+  while (512 * w * c < k) c *= 2;
+  if (c > 4) return {0, 0, 1, kRowThreads};
+  return {w, c, w < 4 ? 4 / w : 1, w > 4 ? kWave * w : kRowThreads};
+}
+
+template <int DT, bool NORM, int W>
+static auto row_kernel_of(int chunks) -> void (*)(RowArgs) {
+  if constexpr (W == 16)
+    if (chunks == 4) return rows_kernel<DT, NORM, W, 4>;
+  return chunks == 1 ? rows_kernel<DT, NORM, W, 1> : rows_kernel<DT, NORM, W, 2>;
+}
+template <int DT, bool NORM>
+static auto row_kernel_of(const RowShape& s) -> void (*)(RowArgs) {
+  switch (s.waves) {
+    case 0: return long_rows_kernel<DT, NORM>;
+    case 1: return row_kernel_of<DT, NORM, 1>(s.chunks);
+    case 4: return row_kernel_of<DT, NORM, 4>(s.chunks);
+    default: return row_kernel_of<DT, NORM, 16>(s.chunks);
+  }
+}
+static auto row_kernel_of(qr_dtype dtype, bool norm, const RowShape& s) -> void (*)(RowArgs) {
+  if (dtype == QR_FP16) return norm ? row_kernel_of<kFp16, true>(s) : row_kernel_of<kFp16, false>(s);
+  return norm ? row_kernel_of<kBf16, true>(s) : row_kernel_of<kBf16, false>(s);
+}
+
 static qr_status launch_rows(qr_dtype dtype, bool norm, const RowArgs& args, hipStream_t st) {
-  return in_launches(args.rows, 1, kRowThreads, [&](long long first, long long count) {
+  const RowShape shape = row_shape(args.rows, args.k);
+  return in_launches(args.rows, shape.rows, shape.threads, [&](long long first, long long count) {
     RowArgs a = args;
     a.x += 2 * first * a.ldx;
     if (a.residual) a.residual += 2 * first * a.ldr;
@@ -669,9 +830,7 @@ static qr_status launch_rows(qr_dtype dtype, bool norm, const RowArgs& args, hip
       a.scales += first;
     }
     a.rows = (int)count;
-    auto kernel = dtype == QR_FP16 ? (norm ? rows_kernel<kFp16, true> : rows_kernel<kFp16, false>)
-                                   : (norm ? rows_kernel<kBf16, true> : rows_kernel<kBf16, false>);
-    return launch_1d(kernel, count, kRowThreads, st, a);
+    return launch_1d(row_kernel_of(dtype, norm, shape), (count + shape.rows - 1) / shape.rows, shape.threads, st, a);
   });
 }
 

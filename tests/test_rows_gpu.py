@@ -45,7 +45,8 @@ def strided(x, off, pad=3):
 # ---------------------------------------------------------------------------
 
 SIZES = [(1, 1), (1, 7), (3, 8), (2, 9), (5, 127), (4, 128), (7, 129), (3, 500), (2, 1000), (6, 2048), (5, 2049), (3, 4096),
-         (2, 4104), (3, 5003), (2, 8192), (2, 8195), (1, 16384), (2, 16391), (1, 32768), (1, 33001), (1, 130944), (300, 70)]
+         (2, 4104), (3, 5003), (2, 8192), (2, 8195), (1, 16384), (2, 16391), (1, 32768), (1, 33001), (1, 130944), (300, 70), (700, 300), (600, 513),
+         (530, 1030), (520, 4095), (515, 4100)]
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))
@@ -159,7 +160,8 @@ def test_norm_of_rows_whose_squares_leave_the_range(qa):
     """bf16 has fp32's range and its squares do not: 2^120 and 2^-120 have their norm, beside ordinary rows."""
     for k in (3, 1000, 40000):
         w = values(1, k, "bf16", 3)[0]
-        x = torch.cat([values(1, k, "bf16", i, s) for i, s in enumerate([1.0, 2.0 ** 118, 2.0 ** 64, 2.0 ** -60, 2.0 ** -118])])
+        x = torch.cat([values(1, k, "bf16", i, s) for i, s in enumerate([1.0, 2.0 ** 118, 2.0 ** 64, 2.0 ** -60, 2.0 ** -118])]
+                      + [torch.full((1, k), v, dtype=torch.bfloat16, device="cuda") for v in (torch.finfo(torch.bfloat16).max, 2.0 ** -130)])
         for eps in (0.0, 1e-6, 2.0 ** -130):
             want, rel = R.norm(f64(x), f64(w), float(np.float32(eps)))
             y, _ = qa.qr_norm(x, w, eps)

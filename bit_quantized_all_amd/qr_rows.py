@@ -62,13 +62,18 @@ def qr_row_bytes(rows, k):
     return _row_bytes(int(rows), int(k))
 
 
-def _on_device(device, fn, *args):
-    """The call with the tensors' device current: a launch goes to the current one."""
-    if torch.cuda.current_device() == device:
-        st = getattr(_lib(), fn)(*args)
+# The current device's number without the checks of torch.cuda.current_device() (a call is microseconds).
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+
+
+def _call(device, fn, *args):
+    """The library's call with the tensors' device current: a launch goes to the current one."""
+    f = getattr(_lib(), fn)
+    if _current_device() == device:
+        st = f(*args)
     else:
         with torch.cuda.device(device):
-            st = getattr(_lib(), fn)(*args)
+            st = f(*args)
     if st:
         _check(fn, st)
 
@@ -86,17 +91,43 @@ def _width(k):
     return -(-k // ROW_RUN) * ROW_RUN
 
 
+def _device(t, name):
+    dev = t.get_device() if isinstance(t, torch.Tensor) else -1
+    if dev < 0:
+        raise ValueError(f"{name} must be a device tensor")
+    return dev
+
+
+def _values(t, name, numel, dtype, device):
+    """Address of a contiguous device tensor of ``numel`` values."""
+    if t.dtype is dtype and t.get_device() == device and t.numel() == numel and t.is_contiguous():
+        return t.data_ptr()
+    return _vector(t, name, numel, dtype, device)     # says what is wrong
+
+
+def _rows(t, name, rows, k, dtype, device):
+    """Address and row stride of a device matrix."""
+    if t.dtype is dtype and t.get_device() == device and t.shape == (rows, k):
+        ld, step = t.stride()
+        if step == 1 and rows > 1 and ld >= k:
+            return t.data_ptr(), ld
+        if rows == 1 and (step == 1 or k == 1):
+            return t.data_ptr(), k
+    return _matrix(t, name, rows, k, device, dtype)   # says what is wrong, if anything is
+
+
 def _codes(t, s, name, device=None):
-    """Addresses of 8-bit rows: contiguous int8 codes [..., whole runs] and fp32 scales."""
-    if not (isinstance(t, torch.Tensor) and t.dtype == torch.int8 and t.dim() >= 2):
+    """Addresses of 8-bit rows, their device and shape: contiguous int8 codes [..., whole runs] and fp32 scales."""
+    dev = _device(t, f"the codes of {name}") if device is None else device
+    shape = t.shape
+    if t.dtype is not torch.int8 or len(shape) < 2:
         raise ValueError(f"the codes of {name} must be int8 rows")
-    if t.shape[-1] % ROW_RUN or not t.shape[-1]:
-        raise ValueError(f"the codes of {name} have rows of {t.shape[-1]}: whole runs of {ROW_RUN}, padded with zeros")
-    cp = _ptr(t, f"the codes of {name}", 0, device)
-    dev = t.get_device()
-    if s.shape != t.shape[:-1]:
-        raise ValueError(f"the scales of {name} are {tuple(s.shape)}, its codes {tuple(t.shape)}")
-    return cp, _vector(s, f"the scales of {name}", s.numel(), torch.float32, dev), dev
+    k = shape[-1]
+    if k % ROW_RUN or not k:
+        raise ValueError(f"the codes of {name} have rows of {k}: whole runs of {ROW_RUN}, padded with zeros")
+    if not t.is_contiguous() or t.get_device() != dev:
+        _ptr(t, f"the codes of {name}", 0, device)
+    return t.data_ptr(), _values(s, f"the scales of {name}", t.numel() // k, torch.float32, dev), dev, shape
 
 
 def _new_codes(like, shape, k, codes, scales, stream, device):
@@ -104,86 +135,96 @@ def _new_codes(like, shape, k, codes, scales, stream, device):
     width, rows = _width(k), math.prod(shape)
     if codes is None:
         codes = _empty(like, (*shape, width), torch.int8, stream)
+        cp = codes.data_ptr()
     elif codes.dtype != torch.int8 or codes.shape != (*shape, width):
         raise ValueError(f"codes is {codes.dtype} {tuple(codes.shape)}, the call needs int8 {(*shape, width)}")
+    else:
+        cp = _ptr(codes, "codes", 0, device)
     if scales is None:
         scales = _empty(like, shape, torch.float32, stream)
-    return codes, scales, _ptr(codes, "codes", 0, device), _vector(scales, "scales", rows, torch.float32, device)
+        sp = scales.data_ptr()
+    else:
+        sp = _vector(scales, "scales", rows, torch.float32, device)
+    return codes, scales, cp, sp
 
 
 def qr_encode_rows(x, codes=None, scales=None, stream=None):
     """8-bit rows of the fp16/bf16 device tensor ``x`` [..., k]: returns (codes int8 [..., k rounded
     up to whole runs of 128], scales fp32 [...]).  A weight [n, k] or [experts, n, k] has a scale for each
     row of n, a matrix of tokens one for each token."""
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() >= 2):
-        raise ValueError("x must be a device tensor of rows")
+    dev = _device(x, "x")
+    if x.dim() < 2:
+        raise ValueError("x must have rows of values")
     dt, k, shape = _dtype(x.dtype), x.shape[-1], x.shape[:-1]
     _width(k)
-    dev, rows = x.get_device(), math.prod(shape)
+    rows = math.prod(shape)
     if x.dim() > 2:
         # a copy, if the dimensions do not merge, is made on the call's stream
         with torch.cuda.stream(stream) if stream is not None else torch.cuda.device(dev):
             x = x.detach().reshape(rows, k)
     ldx = _row_stride(x, "x", rows, k)
     codes, scales, cp, sp = _new_codes(x, shape, k, codes, scales, stream, dev)
-    _on_device(dev, "qr_encode_rows", dt, x.data_ptr(), ldx, cp, sp, rows, k, _stream(stream, dev))
+    _call(dev, "qr_encode_rows", dt, x.data_ptr(), ldx, cp, sp, rows, k, _stream(stream, dev))
     return codes, scales
 
 
 def qr_decode_rows(codes, scales, k, dtype, y=None, stream=None):
     """The values [..., k] of ``dtype`` that 8-bit rows stand for."""
     dt, k = _dtype(dtype), int(k)
-    cp, sp, dev = _codes(codes, scales, "the rows")
-    if _width(k) != codes.shape[-1]:
+    cp, sp, dev, shape = _codes(codes, scales, "the rows")
+    if _width(k) != shape[-1]:
         raise ValueError(f"rows of {codes.shape[-1]} codes do not hold {k} values")
     rows = scales.numel()
     if y is None:
-        y = _empty(codes, (*scales.shape, k), dtype, stream)
+        y = _empty(codes, (*shape[:-1], k), dtype, stream)
         yp, ldy = y.data_ptr(), k
-    elif codes.dim() == 2:
-        yp, ldy = _matrix(y, "y", rows, k, dev, dtype)
+    elif len(shape) == 2:
+        yp, ldy = _rows(y, "y", rows, k, dtype, dev)
     else:
-        if y.dtype != dtype or y.shape != (*scales.shape, k):
-            raise ValueError(f"y is {y.dtype} {tuple(y.shape)}, the call needs {dtype} {(*scales.shape, k)}")
+        if y.dtype != dtype or y.shape != (*shape[:-1], k):
+            raise ValueError(f"y is {y.dtype} {tuple(y.shape)}, the call needs {dtype} {(*shape[:-1], k)}")
         yp, ldy = _ptr(y, "y", 0, dev), k
-    _on_device(dev, "qr_decode_rows", dt, cp, sp, yp, ldy, rows, k, _stream(stream, dev))
+    _call(dev, "qr_decode_rows", dt, cp, sp, yp, ldy, rows, k, _stream(stream, dev))
     return y
 
 
 def _norm(x, weight, eps, residual, total, y, codes, scales, with_output, with_rows, stream):
-    if not (isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2):
+    dev = _device(x, "x")
+    if x.dim() != 2:
         raise ValueError("x must be a device matrix")
-    for t, name in ((x, "x"), (weight, "weight"), (residual, "residual")):
-        if t is not None and t.requires_grad:
-            _no_gradient(t, name)
-    dtype, dev = x.dtype, x.get_device()
+    if x.requires_grad:
+        _no_gradient(x, "x")
+    if weight.requires_grad:
+        _no_gradient(weight, "weight")
+    dtype = x.dtype
     dt = _dtype(dtype)
     rows, k = x.shape
     _width(k)
     if not eps >= 0:
         raise ValueError(f"eps is {eps}, must not be negative")
     ldx = _row_stride(x, "x", rows, k)
-    wp = _vector(weight, "weight", k, dtype, dev)
+    wp = _values(weight, "weight", k, dtype, dev)
     rp = tp = yp = cp = sp = None
     ldr = ldt = ldy = k
     if residual is not None:
-        rp, ldr = _matrix(residual, "residual", rows, k, dev, dtype)
+        if residual.requires_grad:
+            _no_gradient(residual, "residual")
+        rp, ldr = _rows(residual, "residual", rows, k, dtype, dev)
         if total is None:
             total = x.new_empty((rows, k)) if stream is None else _empty(x, (rows, k), dtype, stream)
             tp = total.data_ptr()
         else:
-            tp, ldt = _matrix(total, "total", rows, k, dev, dtype)
+            tp, ldt = _rows(total, "total", rows, k, dtype, dev)
     elif total is not None:
         raise ValueError("total is x itself without a residual")
     if y is not None:
-        yp, ldy = _matrix(y, "y", rows, k, dev, dtype)
+        yp, ldy = _rows(y, "y", rows, k, dtype, dev)
     elif with_output:
         y = x.new_empty((rows, k)) if stream is None else _empty(x, (rows, k), dtype, stream)
         yp = y.data_ptr()
     if with_rows:
         codes, scales, cp, sp = _new_codes(x, (rows,), k, codes, scales, stream, dev)
-    _on_device(dev, "qr_norm", dt, x.data_ptr(), ldx, rp, ldr, wp, eps, tp, ldt, yp, ldy, cp, sp, rows, k,
-               _stream(stream, dev))
+    _call(dev, "qr_norm", dt, x.data_ptr(), ldx, rp, ldr, wp, eps, tp, ldt, yp, ldy, cp, sp, rows, k, _stream(stream, dev))
     return y, total, codes, scales
 
 
@@ -204,33 +245,34 @@ def qr_norm_rows(x, weight, eps=1e-6, residual=None, with_output=False, codes=No
 
 
 def _product8(fn, x, xs, w, ws, dtype, gated, y, offsets, rows, stream):
-    dt = _dtype(dtype)
-    xp, xsp, dev = _codes(x, xs, "x")
-    wp, wsp, _ = _codes(w, ws, "w", dev)
-    dims = 2 if offsets is None else 3
-    if x.dim() != 2 or w.dim() != dims:
-        raise ValueError(f"x must have 2 dimensions and w {dims}, not {x.dim()} and {w.dim()}")
-    tokens, k = x.shape
-    n = w.shape[-2]
-    if w.shape[-1] != k:
-        raise ValueError(f"rows of {k} codes times rows of {w.shape[-1]}")
+    dt = DTYPES.get(dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {dtype}")
+    xp, xsp, dev, xshape = _codes(x, xs, "x")
+    wp, wsp, _, wshape = _codes(w, ws, "w", dev)
+    if len(xshape) != 2 or len(wshape) != (2 if offsets is None else 3):
+        raise ValueError(f"x has 2 dimensions and w {2 if offsets is None else 3}, not {len(xshape)} and {len(wshape)}")
+    tokens, k = xshape
+    n = wshape[-2]
+    if wshape[-1] != k:
+        raise ValueError(f"rows of {k} codes times rows of {wshape[-1]}")
     if gated:
         if n % 2:
             raise ValueError(f"a gated weight has as many gate as up rows, not {n} in all")
         n //= 2
     slots = tokens if rows is None else rows.numel()
     if y is None:
-        y = _empty(x, (slots, n), dtype, stream)
+        y = x.new_empty((slots, n), dtype=dtype) if stream is None else _empty(x, (slots, n), dtype, stream)
         yp, ldy = y.data_ptr(), n
     else:
-        yp, ldy = _matrix(y, "y", slots, n, dev, dtype)
+        yp, ldy = _rows(y, "y", slots, n, dtype, dev)
     if offsets is None:
-        _on_device(dev, fn, dt, gated, xp, xsp, wp, wsp, yp, ldy, slots, n, k, _stream(stream, dev))
+        _call(dev, fn, dt, gated, xp, xsp, wp, wsp, yp, ldy, slots, n, k, _stream(stream, dev))
     else:
-        experts = w.shape[0]
-        op = _vector(offsets, "offsets", experts + 1, torch.int32, dev)
-        rp = None if rows is None else _vector(rows, "rows", slots, torch.int32, dev)
-        _on_device(dev, fn, dt, gated, xp, xsp, tokens, wp, wsp, op, rp, yp, ldy, slots, experts, n, k,
+        experts = wshape[0]
+        op = _values(offsets, "offsets", experts + 1, torch.int32, dev)
+        rp = None if rows is None else _values(rows, "rows", slots, torch.int32, dev)
+        _call(dev, fn, dt, gated, xp, xsp, tokens, wp, wsp, op, rp, yp, ldy, slots, experts, n, k,
                    _stream(stream, dev))
     return y
 
@@ -259,7 +301,8 @@ def qr_choose(logits, top, score="softmax", bias=None, groups=1, top_groups=1, g
     Returns (gates fp32 [tokens, top], ids int32 [tokens, top]): the scores of the chosen, divided by their sum if
     ``renormalise``, times ``factor``.  A logit of -inf or NaN takes its expert out; where fewer than ``top`` are left
     the last ids are -1, with gates of 0, as ``qr_route`` and ``qr_combine`` drop them."""
-    if not (isinstance(logits, torch.Tensor) and logits.is_cuda and logits.dim() == 2):
+    dev = _device(logits, "logits")
+    if logits.dim() != 2:
         raise ValueError("logits must be a device matrix [tokens, experts]")
     dt = LOGIT_DTYPES.get(logits.dtype)
     if dt is None or score not in SCORES:
@@ -269,11 +312,11 @@ def qr_choose(logits, top, score="softmax", bias=None, groups=1, top_groups=1, g
     if bias is not None and bias.requires_grad:
         _no_gradient(bias, "bias")
     tokens, experts = logits.shape
-    top, dev = int(top), logits.get_device()
+    top = int(top)
     if top < 1 or experts < 1:
         raise ValueError(f"no choice of {top} of {experts} experts")
     ldl = _row_stride(logits, "logits", tokens, experts)
-    bp = None if bias is None else _vector(bias, "bias", experts, torch.float32, dev)
+    bp = None if bias is None else _values(bias, "bias", experts, torch.float32, dev)
     if gates is None:
         gates = _empty(logits, (tokens, top), torch.float32, stream)
         gp = gates.data_ptr()
@@ -284,6 +327,6 @@ def qr_choose(logits, top, score="softmax", bias=None, groups=1, top_groups=1, g
         ip = ids.data_ptr()
     else:
         ip = _vector(ids, "ids", tokens * top, torch.int32, dev)
-    _on_device(dev, "qr_choose", dt, SCORES[score], logits.data_ptr(), ldl, bp, int(groups), int(top_groups),
+    _call(dev, "qr_choose", dt, SCORES[score], logits.data_ptr(), ldl, bp, int(groups), int(top_groups),
                int(group_best), bool(renormalise), float(factor), gp, ip, tokens, experts, top, _stream(stream, dev))
     return gates, ids

@@ -252,6 +252,19 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int f = 0; f < NI; ++f) acc[i][f] = i32x4{0, 0, 0, 0};
+  const int c0 = n0 + COLS * wn + 4 * OUT * g;  // the lane's columns of y
+  const float* ws = a.ws + (long long)(rt.zero ? 0 : rt.expert) * HALVES * a.n;
+  float wscale[HALVES][4 * OUT], xscale[MI];
+  int src[MI];  // rows of x of the lane's rows of y
+#pragma unroll
+  for (int q = 0; q < HALVES; ++q)
+#pragma unroll
+    for (int j = 0; j < 4 * OUT; ++j) wscale[q][j] = 0.0f;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) {
+    xscale[i] = 0.0f;
+    src[i] = -1;
+  }
 
   if (!rt.zero) {
     auto place = [](int row) { return (row >> 1) & 7; };
@@ -273,6 +286,12 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
       const int R = 8 * (XI * wave + l) + (lane >> 3), m = rt.m0 + R;
       const long long s = source_row(a, m < rt.m1 ? m : rt.m1 - 1);
       xp[l] = a.x + (s < 0 ? 0 : s) * row_bytes + 16 * ((lane & 7) ^ place(R));
+    }
+    // the scales of the end: asked for here, without branches around their loads, so that nobody waits for them there
+#pragma unroll
+    for (int i = 0; i < MI; ++i) {
+      const int m = rt.m0 + 16 * (MI * wm + i) + r;
+      src[i] = (int)source_row(a, m < rt.m1 ? m : rt.m1 - 1);  // below 2^30
     }
     const uint32_t base = lds_address(&lds[0][0][0]);
     auto fetch = [&](int st, int buf, int l) {
@@ -297,6 +316,13 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
         for (int l = 0; l < LOADS; ++l) fetch(b, b, l);
       }
     }
+    // (a wait for as many loads as were asked for after the first stage's also covers those of the scales)
+#pragma unroll
+    for (int q = 0; q < HALVES; ++q)
+#pragma unroll
+      for (int j = 0; j < 4 * OUT; ++j) wscale[q][j] = ws[q * a.n + (c0 + j < a.n ? c0 + j : a.n - 1)];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) xscale[i] = a.xs[src[i] < 0 ? 0 : src[i]];
     if (NB <= stages) loads_done<(NB - 1) * LOADS>(); else loads_done<0>();
     stage_barrier();
 #pragma unroll
@@ -334,22 +360,6 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
     }
   }
 
-  // the scales, without branches around their loads
-  const int c0 = n0 + COLS * wn + 4 * OUT * g;
-  const float* ws = a.ws + (long long)(rt.zero ? 0 : rt.expert) * HALVES * a.n;
-  float wscale[HALVES][4 * OUT], xscale[MI];
-  bool real[MI];
-#pragma unroll
-  for (int q = 0; q < HALVES; ++q)
-#pragma unroll
-    for (int j = 0; j < 4 * OUT; ++j) wscale[q][j] = ws[q * a.n + (c0 + j < a.n ? c0 + j : a.n - 1)];
-#pragma unroll
-  for (int i = 0; i < MI; ++i) {
-    const int m = rt.m0 + 16 * (MI * wm + i) + r;
-    const long long src = rt.zero ? -1 : source_row(a, m < rt.m1 ? m : rt.m1 - 1);
-    real[i] = src >= 0;
-    xscale[i] = a.xrows ? a.xs[real[i] ? src : 0] : 0.0f;
-  }
 #pragma unroll
   for (int i = 0; i < MI; ++i) {
     const int m = rt.m0 + 16 * (MI * wm + i) + r;
@@ -363,7 +373,7 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
       for (int j = 0; j < 4; ++j) {
         const float q = scaled(acc[i][p][j], xscale[i], wscale[0][4 * p + j]);
         v[j] = GATED ? gate(q, scaled(acc[i][NI - OUT + p][j], xscale[i], wscale[HALVES - 1][4 * p + j])) : q;
-        if (!real[i]) v[j] = 0.0f;
+        if (src[i] < 0) v[j] = 0.0f;
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j) {

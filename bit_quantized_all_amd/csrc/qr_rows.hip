@@ -777,30 +777,34 @@ static qr_status in_launches(long long rows, int per, int threads, LAUNCH launch
 }
 
 // How a row is shared out: by W waves of C chunks a lane, a workgroup of fewer than four waves holding several.
-// Two chunks a lane, one where there are few rows, and as few waves as that takes (us, bf16 with a residual, W x C):
-//   1 x 4096              1x8 6.8    4x2 3.4    16x1 3.0
-//   16 x 8192             4x4 4.8    16x1 3.5
-//   1000 x 2048           1x4 7.0    4x1 4.6    16x1 7.9
-//   65536 x 1024          1x2 52     4x1 83     16x1 270     (without a residual)
-//   32768 x 4096          1x8 235    4x2 189    16x1 245
-//   8192 x 8192, 8 bits   4x4 136    16x1 129
+// Few waves of some chunks where there are many rows, one chunk a lane where there are few (us, bf16, W x C; the
+// last three: to 8-bit rows and back):
+//   norm, residual   1 x 4096       1x8 6.8    4x2 3.4    16x1 3.0
+//                    16 x 8192                 4x4 4.8    16x1 3.5
+//                    1000 x 2048    1x4 7.0    4x1 4.6    16x1 7.9
+//                    32768 x 4096   1x8 235    4x2 189    16x1 245
+//                    20000 x 8192              4x4 237    16x1 225
+//   norm             65536 x 1024   1x2 52     4x1 83     16x1 270
+//   rows             777 x 5003                4x3 9.2    16x1 10.7
+//                    20000 x 5120              4x3 120    16x1 152
+//                    20000 x 7168              4x4 162    16x1 166
 // Rows of over 32768 values are read again for each of a norm's steps.
 struct RowShape {
   int waves, chunks, rows, threads;  // rows: of a workgroup; waves == 0: long rows
 };
 static RowShape row_shape(long long rows, int k) {
-  const int most = rows <= 512 ? 1 : 2;
-  const int w = k <= 512 * most ? 1 : k <= 2048 * most ? 4 : 16;
-  int c = 1;
-  while (512 * w * c < k) c *= 2;
+  const int w = rows <= 512 ? (k <= 512 ? 1 : k <= 2048 ? 4 : 16) : (k <= 1024 ? 1 : k <= 7168 ? 4 : 16);
+  const int c = (k + 512 * w - 1) / (512 * w);
   if (c > 4) return {0, 0, 1, kRowThreads};
   return {w, c, w < 4 ? 4 / w : 1, w > 4 ? kWave * w : kRowThreads};
 }
 
 template <int DT, bool NORM, int W>
 static auto row_kernel_of(int chunks) -> void (*)(RowArgs) {
-  if constexpr (W == 16)
+  if constexpr (W > 1) {
+    if (chunks == 3) return rows_kernel<DT, NORM, W, 3>;
     if (chunks == 4) return rows_kernel<DT, NORM, W, 4>;
+  }
   return chunks == 1 ? rows_kernel<DT, NORM, W, 1> : rows_kernel<DT, NORM, W, 2>;
 }
 template <int DT, bool NORM>

@@ -46,7 +46,7 @@ def strided(x, off, pad=3):
 
 SIZES = [(1, 1), (1, 7), (3, 8), (2, 9), (5, 127), (4, 128), (7, 129), (3, 500), (2, 1000), (6, 2048), (5, 2049), (3, 4096),
          (2, 4104), (3, 5003), (2, 8192), (2, 8195), (1, 16384), (2, 16391), (1, 32768), (1, 33001), (1, 130944), (300, 70), (700, 300), (600, 513),
-         (530, 1030), (520, 4095), (515, 4100)]
+         (530, 1030), (520, 4095), (515, 4100), (514, 7000), (513, 7169), (513, 20000)]
 
 
 @pytest.mark.parametrize("dtype", sorted(DT))

@@ -35,8 +35,8 @@ static qr_status launch_few(int rows, const Product8Args& a, hipStream_t st) {
   }
   if (area >= 2816) {
     // 48 rows a tile where that takes no more of them: 137 rows of 5003 x 4129 18.1 us and 20.0, 96 of 8192 x 8192
-    // 28.8 and 32.4
-    if (!a.offsets && (a.slots + 47) / 48 == (a.slots + 63) / 64) return launch_fragments<DT, GATED, 3, 4>(a, st);
+    // 28.8 and 32.4.  (At most 256 workgroups come here without groups: see launch_dtype.)
+    if (!a.offsets && (a.slots + 47) / 48 == (a.slots + 63) / 64) return launch_fragments<DT, GATED, 3, 4, 8>(a, st);
     return launch_fragments<DT, GATED, 4, 4>(a, st);
   }
   if (area >= 1408) return launch_fragments<DT, GATED, 2, 4>(a, st);

@@ -68,7 +68,8 @@ qr_status qr_decode_rows(qr_dtype dtype, const int8_t *codes, const float *scale
  *   x         device, `rows` rows of k values of `dtype`, row stride ldx
  *   residual  device, the same with row stride ldr; NULL: h = x
  *   weight    device, k values of `dtype`
- *   eps       >= 0 (QR_ERR_ARG otherwise, NaN included)
+ *   eps       >= 0 (QR_ERR_ARG otherwise, NaN included); with 0 a row of zeros is
+ *             NaN, as 0 / 0 is
  *   total     device, row stride ldt, written: h rounded to the dtype, which the
  *             next norm takes as its residual; NULL to leave it (without a
  *             residual it has to be: QR_ERR_ARG).  May be x or residual itself,

@@ -620,17 +620,16 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
       one = larger(one, o);
     }
     const K value = a.best == 2 && two > none ? one + two : one;
-    // A group is kept if fewer than top_groups come before it, counted by their lanes; two values may be off by
-    // twice as much as two ranks.
+    // A group is kept if fewer than top_groups come before it; two values may be off by twice as much as two ranks.
     const float near_by = 2.0f * slack + 0x1p-20f * (float)value;
     int before = 0;
     bool near = false;
-    const int group = lane >> a.span_bits;
-    auto look = [&](auto N) {
-      const K o = row_ror<decltype(N)::value>(value);
-      const int other = ((lane - decltype(N)::value) & (kChooseLanes - 1)) >> a.span_bits;
-      before += o > value || (o == value && other < group);
-      if (!kExact) near |= other != group && fabsf((float)(value - o)) <= near_by;
+    auto look = [&](auto N) {  // at the group of the lane that many below, around the row
+      constexpr int n = decltype(N)::value;
+      if (n & ((1 << a.span_bits) - 1)) return;  // the same for the whole launch
+      const K o = row_ror<n>(value);
+      before += (int)(o > value) | ((int)(o == value) & (int)(lane >= n));
+      if (!kExact) near |= fabsf((float)(value - o)) <= near_by;
     };
     auto all = [&](auto... n) { (look(n), ...); };
     all(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{},
@@ -638,7 +637,6 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
         std::integral_constant<int, 7>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 9>{},
         std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{}, std::integral_constant<int, 12>{},
         std::integral_constant<int, 13>{}, std::integral_constant<int, 14>{}, std::integral_constant<int, 15>{});
-    before >>= a.span_bits;
     const bool kept = before < a.top_groups && value > none;
     if (!kExact) open = by_score && before == a.top_groups - 1 && near;
 #pragma unroll
@@ -670,15 +668,12 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
     // the first of the row's lanes that has it, and there the first
     const uint32_t has = (uint32_t)(__ballot(m == most && !done) >> (16 * row)) & 0xffffu;
     const bool mine = (int)__builtin_ctz(has | 0x10000u) == lane;
-    bool found = !mine;
-    int at = 0;
+    int at = V;
 #pragma unroll
-    for (int v = 0; v < V; ++v) {
-      const bool this_one = !found && k[v] == most;
-      at = this_one ? v : at;
-      k[v] = this_one ? none : k[v];
-      found |= this_one;
-    }
+    for (int v = V - 1; v >= 0; --v) at = k[v] == most ? v : at;
+    at = mine ? at : -1;
+#pragma unroll
+    for (int v = 0; v < V; ++v) k[v] = at == v ? none : k[v];
     if (mine) chosen[j] = V * lane + at;
     count += !done;
   }

@@ -11,7 +11,15 @@ Each rank holds a slice of every expert's hidden width.  A rank's part of the la
 and then the ranks' partial outputs are added up as a compressed all-reduce does:
 ``qr_encode`` on every rank, ``qr_reduce_compressed`` on the encoded buffers.
 
-    python examples/tensor_parallel_moe.py [--tokens T] [--ranks R] [--fmt int4|asym4|fp4]
+With ``--fmt rows8`` weights and activations are held in rows of 8 bits, and the layer begins
+with the norm and the router's choice:
+
+    qr_norm_rows(x, residual)                 the tokens as 8-bit rows, and the next residual
+    qr_choose(logits)                         experts and gates of each token
+    h    = qr_experts8(x, w1, gated)
+    y    = qr_experts8(qr_encode_rows(h), w2)
+
+    python examples/tensor_parallel_moe.py [--tokens T] [--ranks R] [--fmt int4|asym4|fp4|rows8]
 """
 import argparse
 import os
@@ -49,6 +57,33 @@ def layer(ranks, x, ids, gates, experts, wire="int8"):
     return out.view_as(x)
 
 
+class Rank8:
+    """One rank's weights in 8-bit rows: columns [lo, hi) of the hidden width of each expert."""
+
+    def __init__(self, gate_up, down, lo, hi):
+        inner = down.shape[2]
+        rows = torch.cat([torch.arange(lo, hi), torch.arange(inner + lo, inner + hi)])
+        self.w1 = qa.qr_encode_rows(gate_up[:, rows.to(gate_up.device)].contiguous())
+        self.w2 = qa.qr_encode_rows(down[:, :, lo:hi].contiguous())
+
+    def partial(self, codes, scales, dtype, plan, gates):
+        offsets, rows, pos = plan
+        h = qa.qr_experts8(codes, scales, *self.w1, offsets, dtype, rows=rows, gated=True)
+        y = qa.qr_experts8(*qa.qr_encode_rows(h), *self.w2, offsets, dtype)
+        return qa.qr_combine(y, pos, gates)
+
+
+def layer8(ranks, x, residual, weight, router, bias, top, wire="int8"):
+    """Norm, router's choice and experts of the layer on every rank: the output, the next residual, and the choice
+    (the experts by sigmoid score and a bias for balance)."""
+    codes, scales, total, y = qa.qr_norm_rows(x, weight, residual=residual, with_output=True)
+    gates, ids = qa.qr_choose(y @ router, top, score="sigmoid", bias=bias)
+    plan = qa.qr_route(ids, router.shape[1])
+    packed = [qa.qr_encode(wire, r.partial(codes, scales, x.dtype, plan, gates)) for r in ranks]
+    _, out = qa.qr_reduce_compressed(wire, x.dtype, packed, x.numel())
+    return out.view_as(x), total, (gates, ids, y)
+
+
 def reference(gate_up, down, x, ids, gates):
     """The same layer in fp32 with the unpacked weights."""
     out = torch.zeros(x.shape, dtype=torch.float32, device=x.device)
@@ -76,7 +111,7 @@ def main(argv=None):
     ap = argparse.ArgumentParser(description=__doc__.splitlines()[0])
     ap.add_argument("--tokens", type=int, default=512)
     ap.add_argument("--ranks", type=int, default=4)
-    ap.add_argument("--fmt", default="int4", choices=["int4", "asym4", "fp4"])
+    ap.add_argument("--fmt", default="int4", choices=["int4", "asym4", "fp4", "rows8"])
     ap.add_argument("--width", type=int, default=2048)
     ap.add_argument("--inner", type=int, default=1024)
     ap.add_argument("--experts", type=int, default=16)
@@ -86,15 +121,31 @@ def main(argv=None):
         ap.error("inner: a multiple of 128 for each rank; tokens * width: whole tiles of 2048 values")
     x, gate_up, down, ids, gates = make(a.tokens, a.width, a.inner, a.experts, a.top, torch.bfloat16, "cuda")
     part = a.inner // a.ranks
-    ranks = [Rank(a.fmt, gate_up, down, r * part, (r + 1) * part) for r in range(a.ranks)]
-    out = layer(ranks, x, ids, gates, a.experts)
-    want = reference(gate_up, down, x, ids, gates)
+    if a.fmt == "rows8":
+        ranks = [Rank8(gate_up, down, r * part, (r + 1) * part) for r in range(a.ranks)]
+        gen = torch.Generator().manual_seed(1)
+        residual = torch.randn(a.tokens, a.width, generator=gen).to(x)
+        weight = (1 + 0.1 * torch.randn(a.width, generator=gen)).to(x)
+        router = (torch.randn(a.width, a.experts, generator=gen) / a.width ** 0.5).to(x)
+        bias = (0.01 * torch.randn(a.experts, generator=gen)).to(x.device)
+
+        def run():
+            return layer8(ranks, x, residual, weight, router, bias, a.top)
+        out, _, (gates, ids, y) = run()
+        want = reference(gate_up, down, y, ids, gates)
+    else:
+        ranks = [Rank(a.fmt, gate_up, down, r * part, (r + 1) * part) for r in range(a.ranks)]
+
+        def run():
+            return layer(ranks, x, ids, gates, a.experts)
+        out = run()
+        want = reference(gate_up, down, x, ids, gates)
     err = ((out.float() - want).norm() / want.norm()).item()
     times = []
     for _ in range(20):
         begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
         begin.record()
-        layer(ranks, x, ids, gates, a.experts)
+        run()
         end.record()
         end.synchronize()
         times.append(begin.elapsed_time(end))

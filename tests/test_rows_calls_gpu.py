@@ -227,3 +227,19 @@ def test_weights_of_more_than_4_gib(qa):
         at = slice(int(off[e]), int(off[e + 1]))
         check(y[at], x[at], xs[at], w[e], ws[e], False, "bf16", e)
     check(big[::29], x[::29], xs[::29], w[-1], ws[-1], False, "bf16", "last expert")
+
+
+@pytest.mark.parametrize("fmt,bound", [("rows8", 0.055), ("int4", 0.25)])
+def test_example_runs(fmt, bound):
+    """The layer over simulated ranks against the same layer in fp32.  8-bit rows, relative to root mean squares: a row of
+    2048 normal values has a step of its largest, near 3.5, over 127, and uniform errors of 0.8 %, in x and in the weights:
+    1.1 % of the first product, 1.6 % of its gate times up; those products reach 8 to 10, errors of 1.8 to 2.3 %; with the
+    second weight's 0.8 % and the 8-bit wire's 0.5 % twice 2.7 %, and twice that as the bound.  4 bits: as where the layer
+    over them is tested."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "tensor_parallel_moe.py")
+    spec = importlib.util.spec_from_file_location("tensor_parallel_moe", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(["--tokens", "64", "--ranks", "2", "--fmt", fmt]) < bound

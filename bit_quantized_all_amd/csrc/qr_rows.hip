@@ -517,6 +517,24 @@ __device__ __forceinline__ K row_sum(K v) {
   return v + row_ror<1>(v);
 }
 
+// Batcher's odd-even merge sort, the largest first.  V is a power of two.
+template <typename K, int V>
+__device__ __forceinline__ void sort_down(K (&k)[V]) {
+#pragma unroll
+  for (int p = 1; p < V; p *= 2)
+#pragma unroll
+    for (int d = p; d >= 1; d /= 2)
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        // i is the upper of a pair: pairs of blocks of d that begin at d % p, both in the same run of 2 p
+        if (i >= d % p && (i - d % p) / d % 2 == 0 && i + d < V && i / (2 * p) == (i + d) / (2 * p)) {
+          const K most = larger(k[i], k[i + d]);
+          k[i + d] = smaller(k[i], k[i + d]);
+          k[i] = most;
+        }
+      }
+}
+
 // V neighbouring values of a row of `n` from value V lane on, `fill` past the end.
 template <int DT, int V>
 __device__ __forceinline__ void load_run(const uint8_t* row, int lane, int n, float fill, float (&k)[V]) {
@@ -645,38 +663,53 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
 #pragma unroll
     for (int v = 0; v < V; ++v) k[v] = l[v];
   }
-  chosen[lane] = -1;
-  K last = 0;
+  K sorted[V], last = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v) sorted[v] = k[v];
+  sort_down(sorted);
   // With a bias, in fp32, it goes on until a rank is clearly below the one before it, and the top-th at least.
   const bool ahead = a.bias && !kExact;
   bool done = false, sort = false;
-  int count = 0;
+  int count = 0, before_from = -1, again = 0;
+  int from = -1, nth = 0;  // lane j: the j-th chosen is the nth of its value in lane `from`
+  K value = none;
   for (int j = 0; j < (ahead ? kChooseLanes : a.top); ++j) {
-    K m = k[0];
-#pragma unroll
-    for (int v = 1; v < V; ++v) m = larger(m, k[v]);
-    const K most = row_max(m);
+    const K most = row_max(sorted[0]);
     done |= !(most > none);
+    const bool equal = last == most;
     if (ahead) {
       // (NaN, of two ranks of +inf, is not clear)
       const bool clear = (float)(last - most) > slack + 0x1p-21f * fabsf((float)most);
       done |= j >= a.top && clear;
       sort |= !done && j && !clear;
-      last = most;
     }
+    last = most;
     if (__all(done)) break;
-    // the first of the row's lanes that has it, and there the first
-    const uint32_t has = (uint32_t)(__ballot(m == most && !done) >> (16 * row)) & 0xffffu;
-    const bool mine = (int)__builtin_ctz(has | 0x10000u) == lane;
-    int at = V;
+    // the first of the row's lanes that has it
+    const uint32_t has = (uint32_t)(__ballot(sorted[0] == most) >> (16 * row)) & 0xffffu;
+    const int winner = __builtin_ctz(has | 0x10000u);
+    again = equal && winner == before_from ? again + 1 : 0;
+    before_from = winner;
+    if (lane == j && !done) {
+      from = winner;
+      nth = again;
+      value = most;
+    }
+    const bool mine = winner == lane;
 #pragma unroll
-    for (int v = V - 1; v >= 0; --v) at = k[v] == most ? v : at;
-    at = mine ? at : -1;
-#pragma unroll
-    for (int v = 0; v < V; ++v) k[v] = at == v ? none : k[v];
-    if (mine) chosen[j] = V * lane + at;
+    for (int v = 0; v < V && v < kChooseLanes; ++v) {
+      const K here = sorted[v], next = v + 1 < V ? sorted[v + 1] : none;  // values: a choice of elements would be an index
+      sorted[v] = mine ? next : here;
+    }
     count += !done;
   }
+  // Where it lies in that lane: the first of its value, the nth where there are several.
+  uint32_t places = 0;
+#pragma unroll
+  for (int v = 0; v < V; ++v)
+    places |= __shfl(k[v], (threadIdx.x & 48) + (from & 15)) == value ? 1u << v : 0u;
+  for (; __any(nth > 0); --nth) places &= nth > 0 ? places - 1 : ~0u;
+  chosen[lane] = from < 0 ? -1 : V * from + __builtin_ctz(places | 0x80000000u);
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
   if constexpr (!kExact) {
     if (ahead && count == kChooseLanes && a.experts > kChooseLanes && !done) open = true;  // nothing clearly below was seen

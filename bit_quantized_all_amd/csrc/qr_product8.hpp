@@ -23,11 +23,13 @@ struct Product8Args : ProductArgs {
   const float* ws;
 };
 
-// A sum times the scales of its two rows.  |sum| < 2^31: 2^-24 of it times the
-// first scale, the largest |x| over 127, stays in the range of fp32, where the sum
-// times the scale might leave it though the result does not.
+// A sum times the scales of its two rows, in the range of fp32 at every step where
+// the result is: |sum| is at least 1, below 2^31, a scale at most 2^121 (the
+// largest |x| over 127).  A small first scale is multiplied as it is, a large one by
+// 2^-32, after which the second may be as small as there are.
 __device__ __forceinline__ float scaled(int sum, float xs, float ws) {
-  return (float)sum * (xs * 0x1p-24f) * ws * 0x1p24f;
+  const bool large = xs > 0x1p64f;
+  return (float)sum * (large ? xs * 0x1p-32f : xs) * ws * (large ? 0x1p32f : 1.0f);
 }
 
 // ---------------------------------------------------------------------------

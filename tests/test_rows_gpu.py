@@ -249,6 +249,23 @@ def test_linear8_writes_only_its_columns(qa):
 
 
 @pytest.mark.parametrize("m", [1, 20, 300])
+@pytest.mark.parametrize("gated", [False, True])
+def test_scales_below_the_normal_range(qa, m, gated):
+    """Scales of rows of the smallest values: exact powers of two, some below fp32's normal range, whose products with
+    the sums are all above it."""
+    n, k = 40, 640
+    x, _ = R.random_rows(m, k, 1)
+    w, _ = R.random_rows(n * (2 if gated else 1), k, 2)
+    for a, b in ((-140, 20), (20, -140), (-110, 0), (0, -110), (-126, 8), (70, -149), (100, -140), (64, -130)):
+        xs, ws = np.full(m, 2.0 ** a, np.float32), np.full(w.shape[0], 2.0 ** b, np.float32)
+        if gated:
+            with np.errstate(over="ignore"):  # (2^140 is infinite)
+                ws[n:] = np.float32(2.0 ** -a) if a < 0 else 1.0  # up rows' products ordinary, the gates' the smallest
+        y = qa.qr_linear8(dev(x), dev(xs), dev(w), dev(ws), torch.bfloat16, gated=gated)
+        R.check_product(y, x, xs, w, ws, gated, "bf16", (m, a, b))
+
+
+@pytest.mark.parametrize("m", [1, 20, 300])
 def test_scales_at_the_ends_of_the_range(qa, m):
     """Largest and smallest scales whose result is in range: nothing on the way leaves it."""
     n, k = 40, 640

@@ -45,6 +45,11 @@ __device__ __forceinline__ float scaled(int sum, float xs, float ws) {
 // the same.  The weight is the unit's A, so that a lane gets four neighbouring
 // columns of one row of y.
 //
+// Bound by memory where the weight is all there is to read (16 rows, gated, n = k =
+// 8192: 27 us, 5 TB/s; 64 tokens of 8 of 64 experts with 1024 x 2048, gated: 53 us, as
+// much), by what a CU takes from L2, 50 bytes a ns, where rows of x are read beside it (137
+// x 5003 x 4129: 462 KB a workgroup, 9 of 18 us), and by latency below (1 x 4096 x 4096: 5.2).
+//
 // Fragments come straight from memory, 64 bytes of 16 rows at a time, the next
 // run's while one is multiplied.  The workgroups begin at different runs: rows lie a
 // power of two apart, and if all of them read the same columns of their rows at the
@@ -217,6 +222,17 @@ __device__ __forceinline__ int count_tiles(const ProductArgs& a) {
 // LDS: a row is 8 units of 16 bytes, unit u of row R at place u ^ (R / 2 % 8), so
 // that 16 lanes that read one unit of 16 rows hit all 64 banks; the lanes that
 // load it take their units in that order.
+//
+// What bounds it is the clock, which the products pull down to 1.9 GHz or so, and
+// what a CU takes from L2, 12 to 14 TB/s in all: 8192 x 8192 x 8192 in 418 to 439 us
+// (2500 to 2630 TOP/s; the unit alone, on such codes, runs at 4280) with the unit
+// busy 67 % of the time; 340 without the loads, 413 without the reads of LDS, 410
+// without the scales and stores, 288 of products alone.  So a tile is as large as
+// registers allow, and the product is 16 x 16 x 64: at 32 x 32 x 32 the unit draws
+// more (3600 TOP/s alone, 484 to 490 us here).  Two buffers of 64 KB, of runs of 128
+// bytes, did better than four or five of 64 bytes (518 to 523, at 32 x 32 x 32), and as
+// well as a ring of five half stages (440); the smaller tiles have three and four, for
+// which there is room.
 //
 // The column fragments of a wave interleave: row 4 q + j of fragment f is column 4
 // OUT q + 4 f + j, so that a lane has 4 OUT neighbours of a row of y and four

@@ -374,7 +374,9 @@ def test_choose(qa, dtype, score, biased):
     for i, (tokens, experts, top, groups, top_groups, best) in enumerate([
             (1, 1, 1, 1, 1, 1), (5, 2, 2, 1, 1, 1), (40, 7, 3, 1, 1, 1), (64, 64, 8, 1, 1, 1), (30, 65, 8, 1, 1, 1), (9, 130, 64, 1, 1, 1),
             (33, 256, 8, 8, 4, 2), (33, 256, 8, 8, 4, 1), (20, 160, 6, 8, 3, 1), (10, 1024, 10, 64, 5, 2), (7, 1000, 64, 4, 2, 2),
-            (25, 72, 5, 3, 2, 2), (12, 128, 4, 64, 3, 1), (12, 512, 8, 16, 1, 2), (300, 48, 4, 6, 6, 2), (3, 1023, 7, 1, 1, 1)]):
+            (25, 72, 5, 3, 2, 2), (12, 128, 4, 64, 3, 1), (12, 512, 8, 16, 1, 2), (300, 48, 4, 6, 6, 2), (3, 1023, 7, 1, 1, 1),
+            (21, 70, 6, 10, 3, 2), (11, 35, 4, 5, 2, 2), (400, 100, 7, 4, 2, 1), (13, 320, 8, 5, 2, 2), (9, 39, 3, 13, 4, 2), (50, 496, 16, 16, 9, 1),
+            (18, 160, 12, 8, 3, 2), (6, 60, 16, 2, 1, 1)]):
         gen = torch.Generator().manual_seed(100 + i)
         logits = (torch.randn(tokens, experts, generator=gen) * 2).to(LOGITS[dtype]).cuda()
         bias = (torch.randn(experts, generator=gen) * 0.2).cuda() if biased else None
@@ -389,10 +391,10 @@ def test_choose(qa, dtype, score, biased):
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("biased", [False, True])
-@pytest.mark.parametrize("groups,top_groups,best", [(1, 1, 1), (8, 3, 2), (8, 2, 1)])
+@pytest.mark.parametrize("groups,top_groups,best", [(1, 1, 1), (8, 3, 2), (8, 2, 1), (5, 3, 2), (10, 4, 1)])
 def test_choose_masks_ties_and_extremes(qa, score, biased, groups, top_groups, best):
     """Rows without any expert, with fewer than top, of equal logits, and of values at the ends of the range."""
-    E, top = 64, 6
+    E, top = 64 if 64 % groups == 0 else 70, 6
     inf = float("inf")
     gen = torch.Generator().manual_seed(3)
     l = torch.randn(16, E, generator=gen)
@@ -429,16 +431,17 @@ def test_choose_masks_ties_and_extremes(qa, score, biased, groups, top_groups, b
     assert (ids[:2] == -1).all() and not gates[:2].any()
 
 
-def test_choose_close_ranks(qa):
+@pytest.mark.parametrize("E,choices", [(256, ((1, 1, 1), (8, 4, 2), (8, 4, 1))), (200, ((1, 1, 1), (10, 4, 2), (5, 2, 1), (4, 2, 2)))])
+def test_choose_close_ranks(qa, E, choices):
     """Ranks that fp32 cannot tell apart are in the order of 64 bits."""
-    E, tokens = 256, 200
+    tokens = 200
     gen = torch.Generator().manual_seed(5)
     l = torch.randn(tokens, E, generator=gen)
     p = torch.sigmoid(l[0].double())
     l[:] = l[0]
     l[1:] += torch.randint(-2, 3, (tokens - 1, E), generator=gen) * 2.0 ** -23
     bias = (0.7 - p).float()                       # score + bias is 0.7 up to the bias's rounding
-    for groups, top_groups, best in ((1, 1, 1), (8, 4, 2), (8, 4, 1)):
+    for groups, top_groups, best in choices:
         check_choice(qa, l.cuda(), 8, "close", score="sigmoid", bias=bias.cuda(), groups=groups, top_groups=top_groups, best=best)
     s = torch.softmax(l[0].double(), 0)
     check_choice(qa, l.cuda(), 8, "close softmax", score="softmax", bias=(0.01 - s).float().cuda())

@@ -127,6 +127,8 @@ def _codes(t, s, name, device=None):
         raise ValueError(f"the codes of {name} have rows of {k}: whole runs of {ROW_RUN}, padded with zeros")
     if not t.is_contiguous() or t.get_device() != dev:
         _ptr(t, f"the codes of {name}", 0, device)
+    if s.requires_grad:
+        _no_gradient(s, f"a scale of {name}")
     return t.data_ptr(), _values(s, f"the scales of {name}", t.numel() // k, torch.float32, dev), dev, shape
 
 

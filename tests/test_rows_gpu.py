@@ -564,5 +564,18 @@ def test_gradients_are_not_lost_in_silence(qa):
         qa.qr_choose(logits, 2)
     with torch.no_grad():
         assert not qa.qr_choose(logits, 2)[0].requires_grad
+    with pytest.raises(ValueError, match="gradient"):
+        qa.qr_choose(logits.detach(), 2, bias=logits[0].detach().requires_grad_())
     p = torch.nn.Parameter(torch.randn(8, 64, device="cuda").half())
     assert not qa.qr_encode_rows(p)[1].requires_grad
+    codes, scales = qa.qr_encode_rows(x)
+    learned = scales.clone().requires_grad_()
+    offsets = torch.tensor([0, 4], dtype=torch.int32, device="cuda")
+    for call in (lambda: qa.qr_decode_rows(codes, learned, 64, torch.bfloat16),
+                 lambda: qa.qr_linear8(codes, learned, codes, scales, torch.bfloat16),
+                 lambda: qa.qr_linear8(codes, scales, codes, learned, torch.bfloat16),
+                 lambda: qa.qr_experts8(codes, scales, codes[None], learned[None], offsets, torch.bfloat16)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+        with torch.no_grad():
+            call()

@@ -214,6 +214,32 @@ __device__ __forceinline__ int count_tiles(const ProductArgs& a) {
   return __builtin_amdgcn_readfirstlane(count);
 }
 
+// The workgroup's tile.  Of groups the launch is an upper bound on the tiles: those that there are are dealt to the XCDs.
+// An XCD's run of them goes through a group in bands of up to kGroupBand row tiles by all columns, which end with the
+// group, so that its weight is read no more often than it has bands (8192 tokens, 2 of 16 experts, gated, 4096 x 4096:
+// 585 us, and 603 with bands of 4 that go on from one group into the next).
+constexpr int kGroupBand = 8;
+template <int BM>
+__device__ __forceinline__ RowTile find_tile(const ProductArgs& a, int& col) {
+  if (!a.offsets) {
+    const TileIndex t = tile_index(blockIdx.x, gridDim.x, a.ntiles);
+    col = t.col;
+    return find_rows<BM>(a, a.tile0 + t.row);
+  }
+  const int here = min(count_tiles<BM>(a) - a.tile0, (int)(gridDim.x / a.ntiles)), total = here * a.ntiles;
+  RowTile rt = {};
+  col = 0;
+  if ((int)blockIdx.x >= total) return rt;
+  const int xcd = blockIdx.x % kXCDs, rest = total % kXCDs;
+  const int t = xcd * (total / kXCDs) + (xcd < rest ? xcd : rest) + blockIdx.x / kXCDs;
+  rt = find_rows<BM>(a, a.tile0 + t / a.ntiles);  // of the same group
+  const int first = max(rt.first - a.tile0, 0), rows = min(rt.first + rt.count - a.tile0, here) - first;  // in this launch
+  const int in = t - first * a.ntiles, band = in / (kGroupBand * a.ntiles), at = in - band * kGroupBand * a.ntiles;
+  const int high = min(rows - band * kGroupBand, kGroupBand);
+  col = at / high;
+  return find_rows<BM>(a, a.tile0 + first + band * kGroupBand + at % high);
+}
+
 // A workgroup of WM x WN waves computes a tile of 16 WM MI rows of x by 16 WN NI
 // rows of the weight, each wave MI x NI fragments.  A stage is one run of 128
 // bytes of every row; it goes to LDS without a stop in registers while the one
@@ -255,14 +281,11 @@ __global__ __launch_bounds__(kWave* WM* WN, 2) void tiles8_kernel(Product8Args a
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wm = wave / WN, wn = wave % WN;
   const int r = lane & 15, g = lane >> 4;
-  // The launch is an upper bound on the tiles of groups: those that there are are dealt to the XCDs.
-  const int rows_here = a.offsets ? min(count_tiles<BM>(a) - a.tile0, (int)(gridDim.x / a.ntiles)) : (int)(gridDim.x / a.ntiles);
-  if ((int)blockIdx.x >= rows_here * a.ntiles) return;
-  const TileIndex ti = tile_index(blockIdx.x, rows_here * a.ntiles, a.ntiles);
-  RowTile rt = find_rows<BM>(a, a.tile0 + ti.row);
+  int col;
+  RowTile rt = find_tile<BM>(a, col);
   if (rt.m0 >= rt.m1) return;
   rt.zero |= a.xrows == 0;  // every row number is out of range then
-  const int n0 = ti.col * (BN / HALVES);
+  const int n0 = col * (BN / HALVES);
   const long long row_bytes = (long long)a.blocks * kRowRun;
 
   i32x4 acc[MI][NI];

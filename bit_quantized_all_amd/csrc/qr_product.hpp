@@ -82,7 +82,6 @@ struct RowTile {
   int expert;
   int m0, m1;  // rows m0 .. m1 - 1 of y (m0 >= m1: nothing to do)
   bool zero;   // rows of no expert: set to zero
-  int first, count;  // the expert's row tiles (where there are groups)
 };
 
 __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? lo : v > hi ? hi : v; }
@@ -94,14 +93,13 @@ __device__ __forceinline__ int clampi(int v, int lo, int hi) { return v < lo ? l
 // below an earlier one counts as that one, so that no two groups share a row
 // and the launch has a tile for every row.
 template <int BM>
-__device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t) {
+__device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t, int* first_of_group = nullptr, int* tiles_of_group = nullptr) {
   RowTile rt;
   rt.zero = false;
   if (!a.offsets) {
     rt.expert = 0;
     rt.m0 = t * BM;
     rt.m1 = a.slots < rt.m0 + BM ? a.slots : rt.m0 + BM;
-    rt.first = rt.count = 0;
     return rt;
   }
   const int lane = threadIdx.x & (kWave - 1);
@@ -140,15 +138,16 @@ __device__ __forceinline__ RowTile find_rows(const ProductArgs& a, int t) {
       rt.zero = rt.expert == a.experts;
       rt.m0 = begin + (t - first) * BM;
       rt.m1 = end < rt.m0 + BM ? end : rt.m0 + BM;
-      rt.first = first;
-      rt.count = __builtin_amdgcn_readlane(mine, l);
+      if (first_of_group) {
+        *first_of_group = first;
+        *tiles_of_group = __builtin_amdgcn_readlane(mine, l);
+      }
       return rt;
     }
     before += __builtin_amdgcn_readlane(upto, kWave - 1);
   }
   rt.expert = a.experts;
   rt.m0 = rt.m1 = 0;
-  rt.first = rt.count = 0;
   return rt;
 }
 

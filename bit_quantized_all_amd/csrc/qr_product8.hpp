@@ -232,8 +232,9 @@ __device__ __forceinline__ RowTile find_tile(const ProductArgs& a, int& col) {
   if ((int)blockIdx.x >= total) return rt;
   const int xcd = blockIdx.x % kXCDs, rest = total % kXCDs;
   const int t = xcd * (total / kXCDs) + (xcd < rest ? xcd : rest) + blockIdx.x / kXCDs;
-  rt = find_rows<BM>(a, a.tile0 + t / a.ntiles);  // of the same group
-  const int first = max(rt.first - a.tile0, 0), rows = min(rt.first + rt.count - a.tile0, here) - first;  // in this launch
+  int begin = 0, tiles = 0;
+  rt = find_rows<BM>(a, a.tile0 + t / a.ntiles, &begin, &tiles);                                 // of the same group
+  const int first = max(begin - a.tile0, 0), rows = min(begin + tiles - a.tile0, here) - first;  // in this launch
   const int in = t - first * a.ntiles, band = in / (kGroupBand * a.ntiles), at = in - band * kGroupBand * a.ntiles;
   const int high = min(rows - band * kGroupBand, kGroupBand);
   col = at / high;

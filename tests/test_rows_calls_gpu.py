@@ -34,7 +34,7 @@ def test_rows_and_norm_of_several_launches(libraries, rows, k):
     assert same(calls(), small(calls))
 
 
-@pytest.mark.parametrize("tokens,experts,top,groups", [(5000, 64, 4, 1), (3001, 256, 8, 8), (700, 1000, 20, 1), (2500, 7, 2, 1)])
+@pytest.mark.parametrize("tokens,experts,top,groups", [(5000, 64, 4, 1), (3001, 256, 8, 8), (700, 1000, 20, 1), (2500, 7, 2, 1), (4000, 160, 6, 8), (3333, 35, 3, 5)])
 def test_choice_of_several_launches(libraries, tokens, experts, top, groups):
     qa, small = libraries
     gen = torch.Generator().manual_seed(tokens)

@@ -660,7 +660,7 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
     }
     const K value = a.best == 2 && two > none ? one + two : one;
     // A group is kept if fewer than top_groups come before it; two values may be off by twice as much as two ranks.
-    const float near_by = 2.0f * slack + 0x1p-20f * (float)value;
+    const float near_by = 2.0f * slack + 0x1p-20f * fabsf((float)value);
     int before = 0;
     bool near = false;
     auto look = [&](auto N) {  // at the group of the lane that many below, around the row

@@ -1,0 +1,44 @@
+"""The router's choice where ranks, or the values of groups, lie nearer to each other than fp32 tells apart, and where biases
+are negative, large or of either sign (MI355X only)."""
+import pytest
+import torch
+
+from test_rows_gpu import check_choice, dev, log, qa  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def test_two_groups_below_zero(qa):
+    """Both groups' largest ranks are -99.5 in fp32; in 64 bits that of the second is larger."""
+    logits = torch.full((1, 8), -3.0)
+    logits[0, 0], logits[0, 4] = 0.0, 1.2e-5
+    bias = torch.full((8,), -100.0)
+    for top in (1, 3):
+        check_choice(qa, logits.cuda(), top, top, score="sigmoid", bias=bias.cuda(), groups=2, top_groups=1, best=1)
+    assert qa.qr_choose(logits.cuda(), 1, score="sigmoid", bias=bias.cuda(), groups=2)[1].item() == 4
+
+
+def near(experts, groups, best, level, score, seed, tokens=200):
+    """Logits and a bias that put the ``best`` first ranks of every group at ``level``, a number or one for each of them,
+    up to the bias's rounding and some 1e-4 of a logit, and all others 0.5 to 2.5 below."""
+    gen = torch.Generator().manual_seed(seed)
+    base, each = torch.randn(experts, generator=gen), experts // groups
+    p = base.double()
+    p = torch.sigmoid(p) if score == "sigmoid" else torch.softmax(p, 0)
+    at = torch.rand(groups, each, generator=gen).argsort(1)[:, :best] + torch.arange(groups)[:, None] * each
+    low = torch.as_tensor(level, dtype=torch.float64).min() - 0.5 - 2 * torch.rand(experts, generator=gen).double()
+    rank = low.clone()
+    rank[at] = torch.as_tensor(level, dtype=torch.float64).expand(groups, best)
+    return base + 1e-4 * torch.randn(tokens, experts, generator=gen), (rank - p).float()
+
+
+SHAPES = [(256, 8, 4, 2), (256, 8, 4, 1), (200, 10, 4, 2), (70, 5, 2, 1), (64, 16, 7, 2), (512, 2, 1, 2), (640, 20, 7, 2)]
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("level", [0.3, -3.0, -50.0, -1000.0, -1e6])
+@pytest.mark.parametrize("E,groups,top_groups,best", SHAPES)
+def test_close_groups(qa, score, level, E, groups, top_groups, best):
+    logits, bias = near(E, groups, best, level, score, E + groups)
+    check_choice(qa, logits.cuda(), top_groups * best, (score, level, E), score=score, bias=bias.cuda(), groups=groups,
+                 top_groups=top_groups, best=best)

@@ -658,17 +658,14 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
       two = larger(larger(two, w), smaller(one, o));
       one = larger(one, o);
     }
-    const K value = a.best == 2 && two > none ? one + two : one;
-    // A group is kept if fewer than top_groups come before it; two values may be off by twice as much as two ranks.
-    const float near_by = 2.0f * slack + 0x1p-20f * fabsf((float)value);
+    const bool both = a.best == 2 && two > none;
+    const K value = both ? one + two : one;
     int before = 0;
-    bool near = false;
     auto look = [&](auto N) {  // at the group of the lane that many below, around the row
       constexpr int n = decltype(N)::value;
       if (n & ((1 << a.span_bits) - 1)) return;  // the same for the whole launch
       const K o = row_ror<n>(value);
       before += (int)(o > value) | ((int)(o == value) & (int)(lane >= n));
-      if (!kExact) near |= fabsf((float)(value - o)) <= near_by;
     };
     auto all = [&](auto... n) { (look(n), ...); };
     all(std::integral_constant<int, 1>{}, std::integral_constant<int, 2>{}, std::integral_constant<int, 3>{},
@@ -676,8 +673,16 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
         std::integral_constant<int, 7>{}, std::integral_constant<int, 8>{}, std::integral_constant<int, 9>{},
         std::integral_constant<int, 10>{}, std::integral_constant<int, 11>{}, std::integral_constant<int, 12>{},
         std::integral_constant<int, 13>{}, std::integral_constant<int, 14>{}, std::integral_constant<int, 15>{});
+    // A group is kept if fewer than top_groups come before it.
     const bool kept = before < a.top_groups && value > none;
-    if (!kExact) open = by_score && before == a.top_groups - 1 && near;
+    if constexpr (!kExact) {
+      // What the value may be off, and as much again: two ranks by 2^-24 of either's magnitude besides slack / 2, and
+      // their sum by as much of its own.  It is open which groups are kept if not all of them are above all others by
+      // what both are off.
+      const float off = slack + 0x1p-22f * (fabsf(one) + (both ? fabsf(two) : 0.0f));
+      const float least = -row_max(kept ? off - value : none), most = row_max(!kept && value > none ? value + off : none);
+      open = by_score && !(most < least);
+    }
 #pragma unroll
     for (int v = 0; v < V; ++v) k[v] = kept ? a.bias ? k[v] : (K)l[v] : none;
   } else if (!a.bias) {

@@ -42,3 +42,19 @@ def test_close_groups(qa, score, level, E, groups, top_groups, best):
     logits, bias = near(E, groups, best, level, score, E + groups)
     check_choice(qa, logits.cuda(), top_groups * best, (score, level, E), score=score, bias=bias.cuda(), groups=groups,
                  top_groups=top_groups, best=best)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("size", [30.0, 1000.0, 3e5])
+@pytest.mark.parametrize("E,groups,top_groups", [(16, 8, 4), (256, 8, 4), (200, 10, 4), (32, 16, 8), (512, 2, 1), (640, 20, 7)])
+def test_groups_whose_ranks_cancel(qa, score, size, E, groups, top_groups):
+    """A group's two first ranks are near +size and -size, their sum is small and as far off in fp32 as they are."""
+    logits, bias = near(E, groups, 2, [size, -size], score, E + groups)
+    check_choice(qa, logits.cuda(), top_groups, (score, size, E), score=score, bias=bias.cuda(), groups=groups, top_groups=top_groups,
+                 best=2)
+    # and against groups whose ranks are small themselves: the error is the other group's
+    other = near(E, groups, 2, [size, -size], score, E + groups)[1].view(groups, -1)
+    plain = near(E, groups, 2, 0.0, score, E + groups)[1].view(groups, -1)
+    other[::2] = plain[::2]
+    check_choice(qa, logits.cuda(), top_groups, (score, size, E, "mixed"), score=score, bias=other.reshape(-1).cuda(), groups=groups,
+                 top_groups=top_groups, best=2)

@@ -658,8 +658,10 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
       two = larger(larger(two, w), smaller(one, o));
       one = larger(one, o);
     }
+    // Of two ranks their mean in fp32, which holds it where their sum is past its range; a second that there is not is 0.
+    const K share = a.best == 2 && !kExact ? (K)0.5 : (K)1;
     const bool both = a.best == 2 && two > none;
-    const K value = both ? one + two : one;
+    const K value = both ? share * one + share * two : share * one;
     int before = 0;
     auto look = [&](auto N) {  // at the group of the lane that many below, around the row
       constexpr int n = decltype(N)::value;
@@ -679,7 +681,7 @@ __device__ __forceinline__ bool choose_in_row(const ChooseArgs& a, const float (
       // What the value may be off, and as much again: two ranks by 2^-24 of either's magnitude besides slack / 2, and
       // their sum by as much of its own.  It is open which groups are kept if not all of them are above all others by
       // what both are off.
-      const float off = slack + 0x1p-22f * (fabsf(one) + (both ? fabsf(two) : 0.0f));
+      const float off = share * slack + share * 0x1p-22f * fabsf(one) + (both ? share * 0x1p-22f * fabsf(two) : 0.0f);
       const float least = -row_max(kept ? off - value : none), most = row_max(!kept && value > none ? value + off : none);
       open = by_score && !(most < least);
     }

@@ -58,3 +58,26 @@ def test_groups_whose_ranks_cancel(qa, score, size, E, groups, top_groups):
     other[::2] = plain[::2]
     check_choice(qa, logits.cuda(), top_groups, (score, size, E, "mixed"), score=score, bias=other.reshape(-1).cuda(), groups=groups,
                  top_groups=top_groups, best=2)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top_groups", [(16, 4, 2), (16, 4, 4), (256, 8, 4), (200, 10, 9), (640, 20, 19)])
+def test_biases_at_the_end_of_the_range(qa, score, E, groups, top_groups):
+    """Two ranks whose sum is past fp32: a mask of the lowest value leaves its experts in, last, and large ones stay apart."""
+    gen = torch.Generator().manual_seed(E)
+    logits = torch.randn(40, E, generator=gen).cuda()
+    each, big = E // groups, torch.finfo(torch.float32).max
+    low = torch.randn(groups, each, generator=gen) * 0.1
+    low[0] = low[2] = -big                                        # whole groups of it
+    mixed = low.clone()
+    mixed[1, 1:] = -big                                           # a group of one other
+    high = low.clone()
+    high[1, :2], high[2, :2], high[3, 0] = torch.tensor([3e38, 1e38]), torch.tensor([3e38, 2e38]), big
+    ends = low.clone()
+    ends[1, 0], ends[3, :2] = float("inf"), torch.tensor([big, big])
+    only = torch.full((groups, each), -big)
+    only[0] = -float("inf")                                       # no expert to be had, before groups of the lowest value
+    kw = dict(score=score, groups=groups, top_groups=top_groups, best=2)
+    for name, bias in (("low", low), ("mixed", mixed), ("high", high), ("ends", ends), ("only", only)):
+        for top in (2, min(16, E)):
+            check_choice(qa, logits, top, (name, top), bias=bias.reshape(-1).cuda(), **kw)

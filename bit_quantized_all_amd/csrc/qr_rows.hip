@@ -793,8 +793,11 @@ __global__ __launch_bounds__(kChooseThreads) void choose_rows_kernel(ChooseArgs 
   largest = row_max(largest);
   int* chosen = lds[wave][row];
   auto logit_at = [&](int e) { return logit<DT>(a, here ? t : (long long)a.tokens - 1, e); };
-  if (__any(choose_in_row<float, V>(a, l, largest, sum, chosen, logit_at) && here))
-    choose_in_row<double, V>(a, l, largest, sum, chosen, logit_at);
+  if (__any(choose_in_row<float, V>(a, l, largest, sum, chosen, logit_at) && here)) {
+    // (All four tokens, for one that is open; the gates keep the sum in fp32, so that they do not depend on the others.)
+    float again = sum;
+    choose_in_row<double, V>(a, l, largest, again, chosen, logit_at);
+  }
   if (!here) return;
   const int mine = lane < a.top ? chosen[lane] : -1;
   const float gate = gate_of(a, mine >= 0 ? logit<DT>(a, t, mine) : none, largest, sum, row_max<float>, row_sum<float>);

@@ -81,3 +81,25 @@ def test_biases_at_the_end_of_the_range(qa, score, E, groups, top_groups):
     for name, bias in (("low", low), ("mixed", mixed), ("high", high), ("ends", ends), ("only", only)):
         for top in (2, min(16, E)):
             check_choice(qa, logits, top, (name, top), bias=bias.reshape(-1).cuda(), **kw)
+
+
+@pytest.mark.parametrize("E,groups,top_groups,best", [(256, 8, 4, 2), (64, 4, 2, 1), (200, 10, 4, 2), (512, 2, 1, 2)])
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renormalise", [False, True])
+def test_a_token_does_not_depend_on_its_neighbours(qa, score, renormalise, E, groups, top_groups, best):
+    """Bit for bit the same beside tokens whose choice fp32 leaves open, which are compared again in 64 bits."""
+    kw = dict(score=score, groups=groups, top_groups=top_groups, group_best=best, renormalise=renormalise)
+    gen = torch.Generator().manual_seed(E)
+    logits = torch.randn(400, E, generator=gen) * 2
+    close, bias = near(E, groups, best, -3.0, score, E, tokens=400)
+    clear = qa.qr_choose(logits.cuda(), 4, bias=bias.cuda(), **kw)
+    for first in range(4):
+        mixed = logits.clone()
+        mixed[first::4] = close[first::4]
+        own = torch.arange(400) % 4 != first
+        got = qa.qr_choose(mixed.cuda(), 4, bias=bias.cuda(), **kw)
+        assert torch.equal(got[0][own], clear[0][own]) and torch.equal(got[1][own], clear[1][own]), first
+        moved = qa.qr_choose(mixed.roll(1, 0).cuda(), 4, bias=bias.cuda(), **kw)
+        assert torch.equal(moved[0].roll(-1, 0), got[0]) and torch.equal(moved[1].roll(-1, 0), got[1])
+    alone = [qa.qr_choose(logits[i:i + 1].cuda(), 4, bias=bias.cuda(), **kw) for i in range(8)]
+    assert torch.equal(torch.cat([g for g, _ in alone]), clear[0][:8]) and torch.equal(torch.cat([i for _, i in alone]), clear[1][:8])

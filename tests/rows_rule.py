@@ -1,9 +1,16 @@
-"""Which product kernel a call of ``qr_linear8`` or ``qr_experts8`` reaches: the rule of ``launch_dtype`` and
-``launch_few`` in ``csrc/qr_product8.hip``, written out once more so that the tests can say (and check) which
-variant each of their cases runs.
+"""Which kernel a call of the operators over 8-bit rows reaches: the rules of ``launch_dtype`` and ``launch_few`` in
+``csrc/qr_product8.hip`` and of ``row_shape`` and ``qr_choose`` in ``csrc/qr_rows.hip``, written out once more so that
+the tests can say (and check) which variant each of their cases runs.
 
+``variant``, of ``qr_linear8`` or ``qr_experts8``:
     ("fragments", MF, NF, KW)     16 MF rows of x by 16 NF of the weight, KW waves along k
     ("tiles", rows, columns)      tiles of rows of x by rows of the weight
+``row_shape``, of ``qr_encode_rows`` or ``qr_norm``:
+    (waves, chunks)               a row in the registers of so many waves, chunks of 8 values a lane
+    ("long",)                     a row that is read again for each step
+``choice``, of ``qr_choose``:
+    ("rows", run, span, per)      16 lanes a token: registers of a lane, lanes of a group and experts of a lane
+    ("wave",)                     a wave a token
 """
 import math
 
@@ -44,3 +51,24 @@ def variant(slots, n, gated, experts=None):
     costs = [(cost(64, 64, 570, 500), 0), (cost(128, 128, 620, 620), 1), (cost(128, 256, 1000, 1000), 2), (cost(256, 256, 1440, 1440), 3)]
     which = min(costs)[1]
     return few(slots, e, dense, n, gated, rows) if which == 0 else ("tiles", *((128, 128), (128, 256), (256, 256))[which - 1])
+
+
+def row_shape(rows, k):
+    if rows <= 512:
+        waves = 1 if k <= 512 else 4 if k <= 2048 else 16
+    else:
+        waves = 1 if k <= 1024 else 4 if k <= 7168 else 16
+    chunks = -(-k // (512 * waves))
+    return (waves, chunks) if chunks <= 4 else ("long",)
+
+
+def choice(experts, groups, top):
+    each, span, run = experts // groups, 16, 1
+    while groups * span > 16 and span > 1:
+        span //= 2
+    held = -(-each // span)
+    while run < held:
+        run *= 2
+    if top > 16 or run > 32 or groups * span > 16:
+        return ("wave",)
+    return ("rows", run, span, run if groups == 1 else held)

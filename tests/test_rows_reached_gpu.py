@@ -3,8 +3,9 @@ reach is checked against the rules, so that no later change of those leaves one 
 import pytest
 import torch
 
+from rows_reference import DT
 from rows_rule import choice, row_shape
-from test_rows_gpu import LOGITS, SIZES, check_choice, log, qa  # noqa: F401
+from test_rows_gpu import LOGITS, SIZES, check_choice, log, qa, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +44,16 @@ def test_choices_reach_every_layout(qa, score, biased):
     assert {v[:3] for v in reached} == layouts | {("wave",)}
     assert {v[1] for v in reached if len(v) > 1 and v[1] != v[3]} == {4, 8, 16, 32}   # lanes that are not full
     assert choice(64, 1, 17) == ("wave",)
+
+
+@pytest.mark.parametrize("dtype", sorted(DT))
+def test_norm_in_place_in_every_shape(qa, dtype):
+    """The sum over the residual or over x, the result over the other one: nobody reads what another lane has written."""
+    for rows, k in SIZES:
+        x, r, w = values(rows, k, dtype, 1), values(rows, k, dtype, 2), values(1, k, dtype, 3)[0]
+        log(f"norm in place {dtype} {rows}x{k} {row_shape(rows, k)}")
+        codes, scales, total, y = qa.qr_norm_rows(x, w, residual=r, with_output=True)
+        for first in (False, True):
+            a, b = x.clone(), r.clone()
+            got = qa.qr_norm_rows(a, w, residual=b, total=a if first else b, y=b if first else a)
+            assert all(torch.equal(p, q) for p, q in zip(got, (codes, scales, total, y))), (rows, k, first)

@@ -216,8 +216,8 @@ __device__ __forceinline__ int count_tiles(const ProductArgs& a) {
 
 // The workgroup's tile.  Of groups the launch is an upper bound on the tiles: those that there are are dealt to the XCDs.
 // An XCD's run of them goes through a group in bands of up to kGroupBand row tiles by all columns, which end with the
-// group, so that its weight is read no more often than it has bands (8192 tokens, 2 of 16 experts, gated, 4096 x 4096:
-// 585 us, and 603 with bands of 4 that go on from one group into the next).
+// group, so that its weight is read no more often than it has bands (8192 tokens, 2 of 16 experts, gated, 4096 x 4096, in
+// turn on one card: 585 us, and 603 with bands of 4 that go on from one group into the next; cards differ by as much, 578 to 600).
 constexpr int kGroupBand = 8;
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const ProductArgs& a, int& col) {
@@ -251,8 +251,8 @@ __device__ __forceinline__ RowTile find_tile(const ProductArgs& a, int& col) {
 // load it take their units in that order.
 //
 // What bounds it is the clock, which the products pull down to 1.9 GHz or so, and
-// what a CU takes from L2, 12 to 14 TB/s in all: 8192 x 8192 x 8192 in 418 to 439 us
-// (2500 to 2630 TOP/s; the unit alone, on such codes, runs at 4280) with the unit
+// what a CU takes from L2, 12 to 14 TB/s in all: 8192 x 8192 x 8192 in 418 to 447 us
+// (2460 to 2630 TOP/s; the unit alone, on such codes, runs at 4280) with the unit
 // busy 67 % of the time; 340 without the loads, 413 without the reads of LDS, 410
 // without the scales and stores, 288 of products alone.  So a tile is as large as
 // registers allow, and the product is 16 x 16 x 64: at 32 x 32 x 32 the unit draws

@@ -209,7 +209,9 @@ __global__ __launch_bounds__(W > 4 ? kWave * W : kRowThreads) void rows_kernel(R
   }
 }
 
-// Rows that are longer than registers hold: read once for each of the squares, the largest value and the result.
+// Rows that are longer than registers hold: read once for each of the squares, the largest value and the result.  A
+// workgroup a row, a load at a time a thread, so bound by latency: 1 x 130944 bf16 to 8-bit rows 50 us, with the norm
+// and a residual 112; 300 x 40000 25 and 48, where the bytes would take 7 and 14.
 template <int DT, bool NORM>
 __global__ __launch_bounds__(kRowThreads) void long_rows_kernel(RowArgs a) {
   __shared__ float lds[kRowThreads / kWave];
@@ -304,6 +306,8 @@ struct DecodeArgs {
 };
 
 // A workgroup a row.  Memory: 32768 x 4096 in 59 us, 403 MB of which the codes are still in the last-level cache.
+// Narrow rows, which leave threads without work, are bound by the number of workgroups (65536 x 128 bf16: 17 us for 25 MB, x 512:
+// 18 for 101 MB), few long ones by latency (1 x 130944: 16).
 template <int DT>
 __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(DecodeArgs a) {
   const long long row = blockIdx.x;
@@ -367,6 +371,11 @@ __device__ __forceinline__ void first_largest(double& v, int& at) {
 //
 // sigmoid(l) = exp(min(l, 0)) / (1 + exp(-|l|)).  Renormalised, every score may take the same factor, so that
 // those of the chosen do not vanish together: the largest of them has exp(0).
+//
+// In fp32, in units of 2^-24 of the gate: the difference of logits d, exp 2, sigmoid's other factor 5 (1 + exp(-|l|) 2,
+// reciprocal 2, product 1), quotient and factor 2; the sum of the chosen, each off by as much, d no more than 4 on
+// average, and 6 additions: 17; the softmax's sum below 7 twice, 4 and V + 4 (see choose_in_row): with V = 32, 54.
+// In all below d + 60.
 template <typename LARGEST, typename SUM>
 __device__ __forceinline__ float gate_of(const ChooseArgs& a, float l, float base, float sum, LARGEST largest_of,
                                          SUM sum_of) {
@@ -490,9 +499,10 @@ __global__ __launch_bounds__(kWave) void choose_kernel(ChooseArgs a) {
 // wave then takes the same steps in 64 bits.  (Without a bias the logits are compared, which is exact.)
 //
 // A lane's ranks are sorted once, without their numbers.  A round takes the largest of the row's 16 first ones, and
-// its lane moves up; the number is looked up by the value at the end.  Bound by vector instructions, which fill 80 %
-// of the time: 32768 tokens, 256 experts, 8 of them from 4 of 8 groups by sigmoid and bias: 24.7 us, 1200 a wave of 4
-// tokens, half of them in the 9 rounds.  (A round that searched all ranks: 28.8; groups compared by branches and the
+// its lane moves up; the number is looked up by the value at the end.  Bound by vector instructions, which fill 86 %
+// of the time: 32768 tokens, 256 experts, 8 of them from 4 of 8 groups by sigmoid and bias: 22.5 us, 1240 a wave of 4
+// tokens, half of them in the 9 rounds; biases of -5, with more tokens that are open, 24.  (A round that searched all
+// ranks: 28.8, where this took 24.7; groups compared by branches and the
 // chosen one found by scalar masks: 32.3; a wave a token, with ranks in LDS in 64 bits: 141.)
 constexpr int kChooseLanes = 16, kChooseThreads = 256;
 
@@ -1092,7 +1102,7 @@ qr_status qr_choose(qr_dtype dtype, qr_score score, const void* logits, size_t l
   args.factor = factor;
   args.each = args.experts / args.groups;
   // A row of 16 lanes where they hold the experts, up to 32 each, a group in 1, 2, 4 ... of them: 32768 tokens of 160
-  // experts in 8 groups 23 us, by a wave a token 107; of 512 in one 35, of 1024 by a wave a token 255.
+  // experts in 8 groups 24 us, by a wave a token 107; 8 of 512 in one 27, with a bias 49, of 1024 by a wave a token 216.
   int span_bits = 4, run = 1;
   while (args.groups << span_bits > kChooseLanes && span_bits > 0) --span_bits;
   const int held = (args.each + (1 << span_bits) - 1) >> span_bits;

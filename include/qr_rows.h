@@ -114,7 +114,11 @@ qr_status qr_experts8(qr_dtype dtype, int gated, const int8_t *x, const float *x
  *   can be had never are).
  *   ids   = the `top` experts of largest rank in the kept groups, largest first
  *   gates = factor * p of these; with `renormalise` p is divided by the sum of the
- *           chosen p, which is done so that p too small for fp32 do not vanish
+ *           chosen p, which is done so that p too small for fp32 do not vanish.
+ *           Computed in fp32, within (d + 60) 2^-24 of a gate whose p is a normal
+ *           fp32 number: d is how far its logit lies below the row's largest, with
+ *           `renormalise` the largest chosen one (QR_SIGMOID: logits count up to 0,
+ *           and without `renormalise` from 0)
  * Ranks and values are compared as they are in 64 bits (without a bias, ranks and
  * the groups' largest ones as the logits are, of which p is an increasing
  * function); ties go to the lower number.  Where fewer than `top` experts can be had, the last ids are -1 and

@@ -217,7 +217,7 @@ __device__ __forceinline__ int count_tiles(const ProductArgs& a) {
 // The workgroup's tile.  Of groups the launch is an upper bound on the tiles: those that there are are dealt to the XCDs.
 // An XCD's run of them goes through a group in bands of up to kGroupBand row tiles by all columns, which end with the
 // group, so that its weight is read no more often than it has bands (8192 tokens, 2 of 16 experts, gated, 4096 x 4096, in
-// turn on one card: 585 us, and 603 with bands of 4 that go on from one group into the next; cards differ by as much, 578 to 600).
+// turn on one card: 585 us, and 603 with bands of 4 that go on from one group into the next; cards differ by more, 570 to 602).
 constexpr int kGroupBand = 8;
 template <int BM>
 __device__ __forceinline__ RowTile find_tile(const ProductArgs& a, int& col) {
